@@ -1,0 +1,410 @@
+"""What the language-model operators are measured on: cases, inputs, plain forms and 64-bit values.
+
+Three groups, each reached through the package's public calls: the embedding
+lookup and its gradient (dense, accumulated, row-sparse), the RMS norm with
+the residual's addition (plain output or e4m3 codes with group scales) and
+its gradient, and distillation from a teacher's top logits (loss, gradient,
+both at once).  Sizes are generic: hidden sizes around a power of two and
+odd ones, vocabularies around 2^15 to 2^17."""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+BYTES = {"bf16": 2, "fp16": 2, "fp32": 4}
+EPS = 1e-6
+E4M3_MAX = 448.0
+
+
+def listed():
+    return [
+        # the tokens of one decoding step of a few requests
+        {"name": "lookup, 8 tokens", "op": "lookup", "type": "bf16", "n": 8, "vocab": 65536, "dim": 4096},
+        # a training micro-batch's tokens
+        {"name": "lookup, 32768 tokens", "op": "lookup", "type": "bf16", "n": 32768, "vocab": 131072, "dim": 4096},
+        # a small model's dense embedding gradient, every size odd
+        {"name": "embedding gradient, odd", "op": "embed_grad", "type": "fp32", "n": 4001, "vocab": 50021, "dim": 1001},
+        # a tied table: the head's gradient is there already, the lookup's is added
+        {"name": "embedding gradient, tied", "op": "embed_grad_add", "type": "bf16", "n": 16384, "vocab": 131072,
+         "dim": 4096},
+        # the row-sparse gradient that a worker sends instead of the dense one
+        {"name": "embedding gradient, rows", "op": "embed_grad_rows", "type": "bf16", "n": 65536, "vocab": 131072,
+         "dim": 2048},
+        # one decoding step before an 8-bit product
+        {"name": "norm to 8 bits, 4 rows", "op": "norm_q8", "type": "bf16", "rows": 4, "dim": 8192, "group": 128,
+         "residual": True},
+        # a training micro-batch before an 8-bit product
+        {"name": "norm to 8 bits, 16384 rows", "op": "norm_q8", "type": "bf16", "rows": 16384, "dim": 4096,
+         "group": 128, "residual": True},
+        # a final norm in full precision, rows that are no multiple of a vector
+        {"name": "norm, odd", "op": "norm", "type": "fp32", "rows": 2999, "dim": 2051, "residual": False},
+        # the backward pass of a block's norm, with the residual stream's own gradient
+        {"name": "norm gradient", "op": "norm_grad", "type": "bf16", "rows": 16384, "dim": 4096, "residual": True},
+        # evaluation of a student on few positions, a long row each
+        {"name": "distillation loss, 16 rows", "op": "distill_loss", "type": "fp16", "rows": 16, "vocab": 131072,
+         "k": 32},
+        # a training micro-batch: loss and the logits' gradient together
+        {"name": "distillation, both", "op": "distill_both", "type": "bf16", "rows": 4096, "vocab": 131072, "k": 64},
+        # the gradient alone from kept sums, full precision, odd sizes
+        {"name": "distillation gradient, odd", "op": "distill_grad", "type": "fp32", "rows": 1021, "vocab": 50021,
+         "k": 7},
+    ]
+
+
+def _span(rng, lo, hi):
+    """A whole number in [lo, hi], spread over its logarithm."""
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["lookup", "embed_grad", "embed_grad_add", "embed_grad_rows", "norm_q8", "norm", "norm_grad",
+                     "distill_loss", "distill_both", "distill_grad"])
+    case = {"op": op, "type": rng.choice(sorted(TYPES))}
+    if op == "lookup" or op.startswith("embed"):
+        dim = _span(rng, 64, 8192)
+        dim = dim if rng.random() < 0.4 else max(64, dim // 64 * 64)
+        most = max(1, (1 << 27) // dim)
+        case |= {"n": _span(rng, 1, min(65536, most)), "vocab": _span(rng, 1000, min(200000, (1 << 28) // dim)), "dim": dim}
+    elif op.startswith("norm"):
+        dim = _span(rng, 64, 16384)
+        dim = dim if rng.random() < 0.4 else max(64, dim // 64 * 64)
+        case |= {"rows": _span(rng, 1, min(65536, (1 << 26) // dim)), "dim": dim, "residual": rng.random() < 0.7}
+        if op == "norm_q8":
+            case["group"] = rng.choice([0, 32, 64, 128])
+    else:
+        vocab = _span(rng, 1000, 200000)
+        vocab = vocab if rng.random() < 0.4 else max(1024, vocab // 64 * 64)
+        case |= {"rows": _span(rng, 1, min(8192, (1 << 27) // vocab)), "vocab": vocab, "k": _span(rng, 1, 128)}
+    return case
+
+
+# ------------------------------------------------------------------ inputs
+def _tokens(case, gen):
+    """Token ids as text has them: the frequency falls with the rank (the
+    logarithm of the rank is uniform), one in 64 places is padding (-1)."""
+    u = torch.rand(case["n"], generator=gen, device="cuda", dtype=torch.float64)
+    tok = (torch.exp(u * math.log(case["vocab"] + 1.0)).to(torch.int64) - 1).clamp_(0, case["vocab"] - 1)
+    pad = torch.randint(0, 64, (case["n"],), generator=gen, device="cuda") == 0
+    return torch.where(pad, -1, tok)
+
+
+def _normal(gen, shape, dtype, sigma=1.0):
+    return torch.randn(shape, generator=gen, device="cuda").mul_(sigma).to(dtype)
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    op, dt = case["op"], TYPES[case["type"]]
+    s = {"case": case}
+    if op == "lookup":
+        s["tokens"] = _tokens(case, gen)
+        s["table"] = _normal(gen, (case["vocab"], case["dim"]), dt, 0.02)
+        s["scale"] = math.sqrt(case["dim"])
+        s["out"] = torch.empty(case["n"], case["dim"], dtype=dt, device="cuda")
+    elif op.startswith("embed"):
+        s["tokens"] = _tokens(case, gen)
+        s["grad"] = _normal(gen, (case["n"], case["dim"]), dt, 1e-2)
+        s["scale"] = math.sqrt(case["dim"])
+        if op == "embed_grad_rows":
+            s["ids"] = torch.full((case["n"],), -1, dtype=torch.int32, device="cuda")
+            s["rows"] = torch.zeros(case["n"], case["dim"], device="cuda")
+            s["count"] = torch.zeros(1, dtype=torch.int32, device="cuda")
+        elif op == "embed_grad_add":
+            s["dtable"] = _normal(gen, (case["vocab"], case["dim"]), torch.float32, 1e-2)
+        else:
+            s["dtable"] = torch.empty(case["vocab"], case["dim"], device="cuda")
+    elif op.startswith("norm"):
+        rows, dim = case["rows"], case["dim"]
+        loud = torch.where(torch.rand(dim, generator=gen, device="cuda") < 0.01, 12.0, 1.0)  # a few loud channels
+        s["w"] = _normal(gen, (dim,), torch.float32, 0.1).add_(1.0).to(dt)
+        s["x"] = torch.randn(rows, dim, generator=gen, device="cuda").mul_(loud).to(dt)
+        if case["residual"]:
+            s["res"] = torch.randn(rows, dim, generator=gen, device="cuda").mul_(2.0 * loud).to(dt)
+        if op == "norm_grad":
+            s["h"] = s.pop("x")
+            ms = s["h"].double().square().mean(1)
+            s["rstd"] = (1.0 / torch.sqrt(ms + EPS)).float()
+            s["dy"] = _normal(gen, (rows, dim), dt, 1e-2)
+            s["dh"] = s.pop("res", None)
+            if s["dh"] is not None:
+                s["dh"] = (s["dh"].float() * 1e-2).to(dt)
+            s["dx"] = torch.empty(rows, dim, dtype=dt, device="cuda")
+            s["dw"] = torch.empty(dim, device="cuda")
+        else:
+            s["h"] = torch.empty(rows, dim, dtype=dt, device="cuda") if case["residual"] else None
+            s["rstd"] = torch.empty(rows, device="cuda")
+            if op == "norm_q8":
+                group = case["group"] or dim
+                s["codes"] = torch.empty(rows, dim, dtype=torch.float8_e4m3fn, device="cuda")
+                s["scales"] = torch.empty(rows, -(-dim // group), device="cuda")
+            else:
+                s["y"] = torch.empty(rows, dim, dtype=dt, device="cuda")
+    else:
+        rows, vocab, k = case["rows"], case["vocab"], case["k"]
+        z = torch.randn(rows, vocab, generator=gen, device="cuda").mul_(2.5)
+        at = torch.randint(0, vocab, (rows, 1), generator=gen, device="cuda")
+        step = torch.randint(1, max(2, vocab // k), (rows, 1), generator=gen, device="cuda")
+        idx = (at + step * torch.arange(k, device="cuda")) % vocab  # k places, all different
+        top = math.log(vocab) + 4.0 - torch.rand(rows, k, generator=gen, device="cuda").mul_(1.5).cumsum(1)
+        z.scatter_(1, idx, top + torch.randn(rows, k, generator=gen, device="cuda"))
+        short = torch.rand(rows, k, generator=gen, device="cuda") < 0.03  # a nucleus with fewer than k tokens
+        s["idx"] = torch.where(short, -1, idx)
+        s["top"] = top.to(dt)
+        s["z"] = z.to(dt)
+        s["T"] = 2.0
+        kept = torch.rand(rows, generator=gen, device="cuda") >= 0.1  # prompt positions carry no loss
+        kept[0] = True
+        s["row_scale"] = kept.float() / kept.sum()
+        s["loss"] = torch.empty(rows, device="cuda")
+        s["lse"] = torch.empty(rows, device="cuda")
+        if op != "distill_loss":
+            s["dz"] = torch.empty(rows, vocab, dtype=dt, device="cuda")
+        if op == "distill_grad":
+            lse = torch.logsumexp(s["z"].double() / s["T"], 1)
+            s["lse"] = torch.where(s["row_scale"] != 0, lse, 0.0).float()
+    return s
+
+
+# ------------------------------------------------------------- plain forms
+def _plain_embed(s, op):
+    tok, scale = s["tokens"], s["scale"]
+    if op == "lookup":
+        ok = (tok >= 0) & (tok < s["table"].shape[0])
+        rows = s["table"][torch.where(ok, tok, 0)].float() * scale
+        s["out"].copy_(torch.where(ok[:, None], rows, 0.0))
+        return s["out"]
+    vocab = s["case"]["vocab"]
+    ok = (tok >= 0) & (tok < vocab)
+    g = torch.where(ok[:, None], s["grad"].float() * scale, 0.0)
+    if op == "embed_grad_rows":
+        key, order = torch.sort(torch.where(ok, tok, vocab), stable=True)
+        first = torch.ones_like(key)
+        first[1:] = (key[1:] != key[:-1]).long()
+        first = torch.where(key < vocab, first, 0)
+        seat = (first.cumsum(0) - 1).clamp(min=0)
+        s["count"].copy_(first.sum().reshape(1))
+        n = key.numel()
+        s["ids"].copy_(torch.full_like(s["ids"], -1).scatter_reduce(0, seat, torch.where(key < vocab, key, -1).int(), "amax"))
+        s["rows"].zero_()
+        s["rows"].index_add_(0, seat, g[order])
+        return s["ids"], s["rows"], s["count"]
+    if op == "embed_grad":
+        s["dtable"].zero_()
+    s["dtable"].index_add_(0, torch.where(ok, tok, 0), g)
+    return s["dtable"]
+
+
+def _plain_norm(s, op):
+    w = s["w"].float()
+    if op == "norm_grad":
+        h, dy, rstd = s["h"].float(), s["dy"].float(), s["rstd"][:, None]
+        u = dy * w
+        xhat = h * rstd
+        dx = rstd * (u - xhat * (u * xhat).mean(1, keepdim=True))
+        if s["dh"] is not None:
+            dx = dx + s["dh"].float()
+        s["dx"].copy_(dx)
+        s["dw"].copy_((dy * xhat).sum(0))
+        return s["dx"], s["dw"]
+    h = s["x"].float()
+    if s["h"] is not None:
+        h = h + s["res"].float()
+        s["h"].copy_(h)
+    rstd = 1.0 / torch.sqrt(h.square().mean(1) + EPS)
+    s["rstd"].copy_(rstd)
+    y = h * rstd[:, None] * w
+    kept = [s["rstd"]] + ([s["h"]] if s["h"] is not None else [])
+    if op == "norm":
+        s["y"].copy_(y)
+        return [s["y"]] + kept
+    rows, dim = y.shape
+    group = s["case"]["group"] or dim
+    parts = s["scales"].shape[1]
+    if parts * group != dim:
+        wide = torch.zeros(rows, parts * group, device=y.device)
+        wide[:, :dim] = y
+        y = wide
+    y = y.view(rows, parts, group)
+    top = y.abs().amax(2)
+    scale = torch.where(top == 0, 0.0, (top / E4M3_MAX).clamp(min=2.0 ** -126))
+    s["scales"].copy_(scale)
+    v = torch.where(scale[:, :, None] == 0, 0.0, y / scale[:, :, None]).clamp(-E4M3_MAX, E4M3_MAX)
+    s["codes"].copy_(v.view(rows, parts * group)[:, :dim])
+    return [s["codes"], s["scales"]] + kept
+
+
+def _plain_distill(s, op):
+    z, T, rs = s["z"].float() / s["T"], s["T"], s["row_scale"]
+    if op == "distill_grad":
+        lse = s["lse"]
+    else:
+        top = z.amax(1, keepdim=True)
+        lse = (z - top).exp().sum(1).log() + top[:, 0]
+        s["lse"].copy_(torch.where(rs != 0, lse, 0.0))
+    ok = (s["idx"] >= 0) & (s["idx"] < z.shape[1])
+    t = torch.where(ok, s["top"].float() / T, -math.inf)
+    tm = t.amax(1, keepdim=True)
+    some = (tm[:, 0] > -math.inf) & (rs != 0)
+    e = torch.where(ok, (t - torch.where(tm > -math.inf, tm, 0.0)).exp(), 0.0)
+    esum = e.sum(1, keepdim=True)
+    p = e / torch.where(some[:, None], esum, 1.0)
+    at = torch.where(ok, s["idx"], 0)
+    out = []
+    if op != "distill_grad":
+        logp = t - tm - esum.log()
+        logq = z.gather(1, at) - lse[:, None]
+        kl = torch.where(ok & (p > 0), p * (logp - logq), 0.0).sum(1)
+        s["loss"].copy_(torch.where(some, rs * kl, 0.0))
+        out = [s["loss"], s["lse"]]
+    if op != "distill_loss":
+        d = (z - lse[:, None]).exp()
+        d.scatter_add_(1, at, -p)
+        s["dz"].copy_(torch.where(some[:, None], d * (rs / T)[:, None], 0.0))
+        out.append(s["dz"])
+    return out
+
+
+def run(s):
+    op = s["case"]["op"]
+    if own:
+        return _own(s, op)
+    if op == "lookup" or op.startswith("embed"):
+        return _plain_embed(s, op)
+    return _plain_norm(s, op) if op.startswith("norm") else _plain_distill(s, op)
+
+
+def _own(s, op):
+    import gradient_compression_distributed_amd as gcq
+
+    if op == "lookup":
+        return gcq.embed_lookup(s["table"], s["tokens"], s["scale"], out=s["out"])
+    if op.startswith("embed"):
+        plan = gcq.embed_sort(s["tokens"], s["case"]["vocab"])
+        if op == "embed_grad_rows":
+            return gcq.embed_grad_rows(s["grad"], plan, s["scale"], ids=s["ids"], rows=s["rows"], count=s["count"])
+        return gcq.embed_grad(s["grad"], plan, s["scale"], out=s["dtable"], accumulate=op == "embed_grad_add")
+    if op == "norm_grad":
+        return gcq.rms_norm_grad(s["dy"], s["h"], s["w"], s["rstd"], dh=s["dh"], dx=s["dx"], dweight=s["dw"])
+    if op == "norm":
+        y, h, rstd = gcq.rms_norm(s["x"], s["w"], EPS, residual=s.get("res"), y=s["y"], h=s["h"], rstd=s["rstd"])
+        return [y, rstd] + ([h] if s["h"] is not None else [])
+    if op == "norm_q8":
+        codes, scales, h, rstd = gcq.rms_norm_q8(s["x"], s["w"], EPS, group=s["case"]["group"], residual=s.get("res"),
+                                                 codes=s["codes"], scales=s["scales"], h=s["h"], rstd=s["rstd"])
+        return [codes, scales, rstd] + ([h] if s["h"] is not None else [])
+    if op == "distill_loss":
+        return gcq.distill_loss(s["z"], s["idx"], s["top"], s["T"], row_scale=s["row_scale"], loss=s["loss"], lse=s["lse"])
+    if op == "distill_grad":
+        return [gcq.distill_grad(s["z"], s["lse"], s["idx"], s["top"], s["T"], row_scale=s["row_scale"], out=s["dz"])]
+    return gcq.distill_loss_grad(s["z"], s["idx"], s["top"], s["T"], row_scale=s["row_scale"], loss=s["loss"],
+                                 lse=s["lse"], out=s["dz"])
+
+
+# --------------------------------------------------------------- the floor
+def _distinct(n, vocab):
+    """The expected number of different tokens among n drawn as _tokens draws them."""
+    edge = np.log(np.arange(1, vocab + 2)) / math.log(vocab + 1.0)
+    return float((1.0 - (1.0 - np.diff(edge) * 63 / 64) ** n).sum())
+
+
+def work(case):
+    op, b = case["op"], BYTES[case["type"]]
+    if op == "lookup" or op.startswith("embed"):
+        n, dim, vocab = case["n"], case["dim"], case["vocab"]
+        u = _distinct(n, vocab)
+        if op == "lookup":
+            return {"bytes": 8 * n + b * dim * (u + n), "flops": n * dim}
+        out = {"embed_grad": 4 * vocab * dim, "embed_grad_add": 8 * u * dim, "embed_grad_rows": 4 * u * dim + 4 * u + 4}[op]
+        return {"bytes": 8 * n + b * n * dim * 63 / 64 + out, "flops": n * dim}
+    if op.startswith("norm"):
+        cells, dim, rows = case["rows"] * case["dim"], case["dim"], case["rows"]
+        extra = 2 if case["residual"] else 0
+        if op == "norm_grad":  # dy, h and dh in, dx out
+            return {"bytes": b * cells * (3 + (1 if case["residual"] else 0)) + b * dim + 4 * dim + 4 * rows, "flops": 9 * cells}
+        if op == "norm":
+            return {"bytes": b * cells * (2 + extra) + b * dim + 4 * rows, "flops": 5 * cells}
+        parts = -(-dim // (case["group"] or dim))
+        return {"bytes": b * cells * (1 + extra) + cells + 4 * rows * parts + b * dim + 4 * rows, "flops": 7 * cells}
+    rows, cells, k = case["rows"], case["rows"] * case["vocab"], case["k"]
+    once = 0.9 * b * cells + rows * (k * (8 + b) + 4)  # nine rows in ten carry a loss
+    if op == "distill_loss":
+        return {"bytes": once + 8 * rows, "flops": 4 * cells}
+    if op == "distill_grad":
+        return {"bytes": once + 4 * rows + b * cells, "flops": 4 * cells}
+    return {"bytes": once + 8 * rows + b * cells, "flops": 8 * cells}
+
+
+# --------------------------------------------------------- 64-bit values
+def _e4m3(v):
+    """The nearest e4m3 value (ties to even), of magnitudes up to 448."""
+    _, e = torch.frexp(v)
+    step = torch.exp2(((e - 1).clamp(min=-6) - 3).double())
+    return torch.round(v / step) * step
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "lookup":
+        out = torch.zeros(case["n"], case["dim"], dtype=torch.float64, device="cuda")
+        real = torch.nonzero(s["tokens"] >= 0)[:, 0]
+        out[real] = s["scale"] * s["table"].double()[s["tokens"][real]]
+        return out
+    if op.startswith("embed"):
+        real = torch.nonzero(s["tokens"] >= 0)[:, 0]
+        tok, g = s["tokens"][real], s["grad"].double()[real]
+        if op == "embed_grad_rows":
+            ids, back = torch.unique(tok, return_inverse=True)
+            rows = torch.zeros(case["n"], case["dim"], dtype=torch.float64, device="cuda")
+            rows.index_put_((back,), g, accumulate=True)
+            return None, rows * s["scale"], None
+        d = torch.zeros(case["vocab"], case["dim"], dtype=torch.float64, device="cuda")
+        d.index_put_((tok,), g, accumulate=True)
+        d *= s["scale"]
+        return d + s["dtable"].double() if op == "embed_grad_add" else d
+    if op.startswith("norm"):
+        w, dim = s["w"].double(), case["dim"]
+        if op == "norm_grad":
+            h, r = s["h"].double(), s["rstd"].double()[:, None]
+            u = s["dy"].double() * w
+            dx = r * u - h * r ** 3 * ((u * h).sum(1, keepdim=True) / dim)
+            if s["dh"] is not None:
+                dx += s["dh"].double()
+            return dx, (s["dy"].double() * h * r).sum(0)
+        h = s["x"].double()
+        if case["residual"]:
+            h = h + s["res"].double()
+        r = (h.pow(2).sum(1) / dim + EPS).rsqrt()
+        y = h * (r[:, None] * w)
+        kept = [r] + ([h] if case["residual"] else [])
+        if op == "norm":
+            return [y] + kept
+        group = case["group"] or dim
+        ends = torch.arange(dim, device="cuda") // group
+        top = torch.zeros(case["rows"], int(ends[-1]) + 1, dtype=torch.float64, device="cuda")
+        top.scatter_reduce_(1, ends.expand_as(y), y.abs(), "amax")
+        scale = (top / E4M3_MAX).clamp(min=2.0 ** -126) * (top > 0)
+        each = scale[:, ends]
+        return [_e4m3(torch.where(each > 0, y / each, torch.zeros_like(y))), scale] + kept
+    T, rs, rows = s["T"], s["row_scale"].double(), case["rows"]
+    z = s["z"].double() / T
+    lse = torch.logsumexp(z, 1) if op != "distill_grad" else s["lse"].double()
+    real = s["idx"] >= 0
+    t = (s["top"].double() / T).masked_fill(~real, -math.inf)
+    some = real.any(1) & (rs != 0)
+    p = torch.where(some[:, None], torch.softmax(t, 1), 0.0)
+    out = []
+    if op != "distill_grad":
+        cross = torch.log(p.clamp(min=1e-300)) - (torch.gather(z, 1, s["idx"].clamp(min=0)) - lse[:, None])
+        out = [rs * (p * cross).sum(1), torch.where(rs != 0, lse, 0.0)]
+    if op != "distill_loss":
+        z -= lse[:, None]
+        z.exp_()
+        r, c = torch.nonzero(real, as_tuple=True)
+        z[r, s["idx"][r, c]] -= p[r, c]
+        out.append(z * torch.where(some, rs / T, 0.0)[:, None])
+    return out
