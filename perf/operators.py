@@ -22,34 +22,34 @@ E4M3_MAX = 448.0
 def listed():
     return [
         # the tokens of one decoding step of a few requests
-        {"name": "lookup, 8 tokens", "op": "lookup", "type": "bf16", "n": 8, "vocab": 65536, "dim": 4096},
+        {"name": "lookup: 8 tokens", "op": "lookup", "type": "bf16", "n": 8, "vocab": 65536, "dim": 4096},
         # a training micro-batch's tokens
-        {"name": "lookup, 32768 tokens", "op": "lookup", "type": "bf16", "n": 32768, "vocab": 131072, "dim": 4096},
+        {"name": "lookup: 32768 tokens", "op": "lookup", "type": "bf16", "n": 32768, "vocab": 131072, "dim": 4096},
         # a small model's dense embedding gradient, every size odd
-        {"name": "embedding gradient, odd", "op": "embed_grad", "type": "fp32", "n": 4001, "vocab": 50021, "dim": 1001},
+        {"name": "embedding gradient: odd", "op": "embed_grad", "type": "fp32", "n": 4001, "vocab": 50021, "dim": 1001},
         # a tied table: the head's gradient is there already, the lookup's is added
-        {"name": "embedding gradient, tied", "op": "embed_grad_add", "type": "bf16", "n": 16384, "vocab": 131072,
+        {"name": "embedding gradient: tied", "op": "embed_grad_add", "type": "bf16", "n": 16384, "vocab": 131072,
          "dim": 4096},
         # the row-sparse gradient that a worker sends instead of the dense one
-        {"name": "embedding gradient, rows", "op": "embed_grad_rows", "type": "bf16", "n": 65536, "vocab": 131072,
+        {"name": "embedding gradient: rows", "op": "embed_grad_rows", "type": "bf16", "n": 65536, "vocab": 131072,
          "dim": 2048},
         # one decoding step before an 8-bit product
-        {"name": "norm to 8 bits, 4 rows", "op": "norm_q8", "type": "bf16", "rows": 4, "dim": 8192, "group": 128,
+        {"name": "norm to 8 bits: 4 rows", "op": "norm_q8", "type": "bf16", "rows": 4, "dim": 8192, "group": 128,
          "residual": True},
         # a training micro-batch before an 8-bit product
-        {"name": "norm to 8 bits, 16384 rows", "op": "norm_q8", "type": "bf16", "rows": 16384, "dim": 4096,
+        {"name": "norm to 8 bits: 16384 rows", "op": "norm_q8", "type": "bf16", "rows": 16384, "dim": 4096,
          "group": 128, "residual": True},
         # a final norm in full precision, rows that are no multiple of a vector
-        {"name": "norm, odd", "op": "norm", "type": "fp32", "rows": 2999, "dim": 2051, "residual": False},
+        {"name": "norm: odd", "op": "norm", "type": "fp32", "rows": 2999, "dim": 2051, "residual": False},
         # the backward pass of a block's norm, with the residual stream's own gradient
         {"name": "norm gradient", "op": "norm_grad", "type": "bf16", "rows": 16384, "dim": 4096, "residual": True},
         # evaluation of a student on few positions, a long row each
-        {"name": "distillation loss, 16 rows", "op": "distill_loss", "type": "fp16", "rows": 16, "vocab": 131072,
+        {"name": "distillation loss: 16 rows", "op": "distill_loss", "type": "fp16", "rows": 16, "vocab": 131072,
          "k": 32},
         # a training micro-batch: loss and the logits' gradient together
-        {"name": "distillation, both", "op": "distill_both", "type": "bf16", "rows": 4096, "vocab": 131072, "k": 64},
+        {"name": "distillation: both", "op": "distill_both", "type": "bf16", "rows": 4096, "vocab": 131072, "k": 64},
         # the gradient alone from kept sums, full precision, odd sizes
-        {"name": "distillation gradient, odd", "op": "distill_grad", "type": "fp32", "rows": 1021, "vocab": 50021,
+        {"name": "distillation gradient: odd", "op": "distill_grad", "type": "fp32", "rows": 1021, "vocab": 50021,
          "k": 7},
     ]
 
