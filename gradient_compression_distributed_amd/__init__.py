@@ -25,6 +25,8 @@ __all__ = [
     "saps_mask", "saps_gather", "saps_merge", "saps_mask_words", "saps_num_tiles",
     "qsgd_elias_encode", "qsgd_elias_decode", "qsgd_elias_max_words",
     "probe_stream", "probe_reduce",
+    "embed_lookup", "embed_sort", "EmbedPlan", "embed_grad", "embed_grad_rows",
+    "embed_plan_words", "embed_work_bytes",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -128,6 +130,18 @@ def load():
     lib.gcq_get_tuning.restype = i32
     lib.gcq_set_tuning.argtypes = [ctypes.POINTER(Tuning)]
     lib.gcq_set_tuning.restype = i32
+    lib.embed_lookup.argtypes = [vp, i32, sz, sz, sz, vp, i32, sz, f32, vp, i32, sz, vp]
+    lib.embed_lookup.restype = i32
+    lib.embed_sort.argtypes = [vp, i32, sz, sz, vp, vp]
+    lib.embed_sort.restype = i32
+    lib.embed_grad.argtypes = [vp, i32, sz, vp, sz, sz, sz, f32, i32, vp, sz, vp, vp]
+    lib.embed_grad.restype = i32
+    lib.embed_grad_rows.argtypes = [vp, i32, sz, vp, sz, sz, sz, f32, vp, vp, sz, vp, vp, vp]
+    lib.embed_grad_rows.restype = i32
+    lib.embed_plan_words.argtypes = [sz]
+    lib.embed_plan_words.restype = sz
+    lib.embed_work_bytes.argtypes = [sz, sz]
+    lib.embed_work_bytes.restype = sz
     _lib = lib
     return lib
 
@@ -518,3 +532,205 @@ def qsgd_elias_decode(words, offsets, n: int, d: int, norms=None, nibbles=None):
     _check(lib.qsgd_elias_decode(_ptr(words), words.numel(), _ptr(offsets), n, d, _ptr(norms),
                                  _ptr(nibbles), _stream(words.device)), "qsgd_elias_decode")
     return norms, nibbles
+
+
+# ------------------------------------------------- language-model operators
+# Matrices are 2-D tensors whose rows are contiguous; rows may lie further
+# apart than their length (a slice of columns).  A call runs on the device of
+# its tensors, on that device's current stream, whatever device is current.
+_type_codes = None
+
+
+def _type_code(x, name, allowed=(0, 1, 2)):
+    """The C ABI's enum gcq_type of a tensor's element type."""
+    global _type_codes
+    if _type_codes is None:
+        import torch
+
+        _type_codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int32: 3,
+                       torch.int64: 4}
+    code = _type_codes.get(x.dtype, -1)
+    if code not in allowed:
+        raise TypeError(f"{name} has type {x.dtype}, which this call does not take")
+    return code
+
+
+def _on(x, name, device=None):
+    """Refuses what is not a GPU tensor (on ``device``, an index, if given);
+    returns the index of its device."""
+    try:
+        at = x.get_device()
+    except AttributeError:
+        raise TypeError(f"{name} must be a torch tensor") from None
+    if at < 0:
+        raise ValueError(f"{name} must live in GPU memory (got {x.device})")
+    if device is not None and at != device:
+        raise ValueError(f"{name} is on device {at}, the call's other tensors on {device}")
+    return at
+
+
+def _matrix(x, name, rows, cols, device, written=False):
+    """Checks a matrix of rows x cols (at least ``rows`` rows if it is
+    written); returns the distance of its rows in elements."""
+    _on(x, name, device)
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != cols or (shape[0] < rows if written else shape[0] != rows):
+        raise ValueError(f"{name} has shape {tuple(shape)}, needs ({rows}, {cols})")
+    ld, step = x.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if shape[0] <= 1:
+        return cols
+    if ld < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return ld
+
+
+def _vector(x, name, n, device, dtype=None, at_least=False):
+    """Checks a contiguous tensor of n elements (or at least n)."""
+    _on(x, name, device)
+    if dtype is not None and x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {x.dtype})")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    have = x.numel()
+    if have < n if at_least else have != n:
+        raise ValueError(f"{name} holds {have} elements, needs {n}")
+
+
+def _call(fn, where, device, *args):
+    """fn(*args, stream) on a device's current stream, with that device
+    current while it runs."""
+    import torch
+
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status != 0:
+        raise GcqError(status, where)
+
+
+def embed_plan_words(n: int) -> int:
+    return int(load().embed_plan_words(n))
+
+
+def embed_work_bytes(n: int, dim: int) -> int:
+    return int(load().embed_work_bytes(n, dim))
+
+
+def embed_lookup(table, tokens, scale: float = 1.0, out=None):
+    """out[i] = scale * table[tokens[i]], rounded once to out's type (the
+    table's by default).  Tokens outside the table are padding: zero rows."""
+    import torch
+
+    lib = load()
+    dev = _on(table, "table")
+    if table.dim() != 2:
+        raise ValueError("table must be a matrix")
+    vocab, dim = table.shape
+    ld = _matrix(table, "table", vocab, dim, dev)
+    n = tokens.numel()
+    _vector(tokens, "tokens", n, dev)
+    if out is None:
+        out = torch.empty((n, dim), dtype=table.dtype, device=table.device)
+    out_ld = _matrix(out, "out", n, dim, dev)
+    _call(lib.embed_lookup, "embed_lookup", dev, table.data_ptr(), _type_code(table, "table"),
+          vocab, dim, ld, tokens.data_ptr(), _type_code(tokens, "tokens", (3, 4)), n, scale,
+          out.data_ptr(), _type_code(out, "out"), out_ld)
+    return out
+
+
+class EmbedPlan:
+    """Positions ordered by token (embed_sort): the plan's words and the
+    sizes they belong to."""
+
+    def __init__(self, words, n: int, vocab: int):
+        self.words, self.n, self.vocab = words, n, vocab
+
+
+def embed_sort(tokens, vocab: int, plan=None) -> EmbedPlan:
+    """The plan of a batch's tokens for embed_grad and embed_grad_rows.  A
+    plan of as many tokens is overwritten if given."""
+    import torch
+
+    lib = load()
+    n = tokens.numel()
+    dev = _on(tokens, "tokens")
+    _vector(tokens, "tokens", n, dev)
+    if plan is None:
+        plan = EmbedPlan(torch.empty(lib.embed_plan_words(n), dtype=torch.int32,
+                                     device=tokens.device), n, vocab)
+    elif plan.n != n:
+        raise ValueError(f"the plan given is for {plan.n} tokens, not {n}")
+    _vector(plan.words, "plan", lib.embed_plan_words(n), dev, torch.int32, at_least=True)
+    _call(lib.embed_sort, "embed_sort", dev, tokens.data_ptr(),
+          _type_code(tokens, "tokens", (3, 4)), n, vocab, plan.words.data_ptr())
+    plan.vocab = vocab
+    return plan
+
+
+def _embed_grad_args(lib, grad, plan, dim, work):
+    import torch
+
+    dev = _on(grad, "grad")
+    ld = _matrix(grad, "grad", plan.n, dim, dev)
+    _vector(plan.words, "plan", lib.embed_plan_words(plan.n), dev, torch.int32, at_least=True)
+    need = lib.embed_work_bytes(plan.n, dim)
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device=grad.device)
+    else:
+        _vector(work, "work", need, dev, torch.uint8, at_least=True)
+    return dev, ld, work
+
+
+def embed_grad(grad, plan: EmbedPlan, scale: float = 1.0, out=None, accumulate: bool = False,
+               work=None):
+    """The table's gradient, float32: out[v] = scale * (sum of grad[i] over
+    the positions i of token v), zero where no token is; with ``accumulate``
+    it is added to out instead."""
+    import torch
+
+    lib = load()
+    dim = grad.shape[-1]
+    dev, ld, work = _embed_grad_args(lib, grad, plan, dim, work)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((plan.vocab, dim), dtype=torch.float32, device=grad.device)
+    out_ld = _matrix(out, "out", plan.vocab, dim, dev)
+    _type_code(out, "out", (0,))
+    _call(lib.embed_grad, "embed_grad", dev, grad.data_ptr(), _type_code(grad, "grad"), ld,
+          plan.words.data_ptr(), plan.n, plan.vocab, dim, scale, accumulate, out.data_ptr(), out_ld,
+          work.data_ptr())
+    return out
+
+
+def embed_grad_rows(grad, plan: EmbedPlan, scale: float = 1.0, ids=None, rows=None, count=None,
+                    work=None):
+    """The same gradient in row-sparse form: (ids int32, rows float32, count
+    int32[1]).  The first ``count`` ids are the batch's different tokens in
+    ascending order and the same rows their gradients; what is behind them is
+    left as it was.  ids and rows hold at least min(n, vocab) entries."""
+    import torch
+
+    lib = load()
+    dim = grad.shape[-1]
+    dev, ld, work = _embed_grad_args(lib, grad, plan, dim, work)
+    most = min(plan.n, plan.vocab)
+    if ids is None:
+        ids = torch.empty(most, dtype=torch.int32, device=grad.device)
+    if rows is None:
+        rows = torch.empty((most, dim), dtype=torch.float32, device=grad.device)
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=grad.device)
+    _vector(ids, "ids", most, dev, torch.int32, at_least=True)
+    _vector(count, "count", 1, dev, torch.int32)
+    rows_ld = _matrix(rows, "rows", most, dim, dev, written=True)
+    _type_code(rows, "rows", (0,))
+    _call(lib.embed_grad_rows, "embed_grad_rows", dev, grad.data_ptr(), _type_code(grad, "grad"),
+          ld, plan.words.data_ptr(), plan.n, plan.vocab, dim, scale, ids.data_ptr(),
+          rows.data_ptr(), rows_ld, count.data_ptr(), work.data_ptr())
+    return ids, rows, count

@@ -420,6 +420,116 @@ int saps_merge(float *x, size_t n, const uint32_t *mask_words, const uint64_t *t
                const float *peer_values, size_t capacity, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Language-model operators: element types and limits                  */
+/* ------------------------------------------------------------------ */
+
+/*
+ * The operators below form and shrink what a language model's training step
+ * holds: the embedding table's gradient (also row-sparse), a norm's output
+ * in 8 bits, a teacher's top logits.  Beyond the conventions above:
+ *   - Matrices are row-major; `ld` is the distance between rows in elements,
+ *     at least the row's length.  Rows and pointers need only their element's
+ *     alignment.
+ *   - 16-bit inputs are widened to float32, sums and statistics are held in
+ *     float32, and an output of 16 or 8 bits is rounded once, to nearest,
+ *     ties to even.  Products and sums may be fused and are taken in a fixed
+ *     order: the same call on the same inputs gives the same bits.
+ *   - An operand's range for the overlap check goes from its first to its
+ *     last element, the gaps between rows included; the gaps are not written.
+ */
+enum gcq_type {
+    GCQ_F32 = 0,
+    GCQ_F16 = 1,
+    GCQ_BF16 = 2,
+    GCQ_I32 = 3,
+    GCQ_I64 = 4
+};
+
+/* Largest row (token) count and row length of the operators below. */
+#define GCQ_LM_MAX_ROWS ((size_t)1 << 30)
+#define GCQ_LM_MAX_DIM ((size_t)1 << 22)
+
+/* ------------------------------------------------------------------ */
+/* Embedding lookup, and its gradient by sorted tokens                 */
+/* ------------------------------------------------------------------ */
+
+/*
+ * embed_lookup -- rows of an embedding table, scaled: for every i < n
+ *     out[i] = scale * table[tokens[i]]     (float32, rounded once)
+ * A token outside [0, vocab) is padding: its row of out is zero.
+ *
+ *   table   in,  vocab x dim of table_type (a float type), rows table_ld apart
+ *   tokens  in,  n of token_type (GCQ_I32 or GCQ_I64)
+ *   scale   finite
+ *   out     out, n x dim of out_type (a float type), rows out_ld apart
+ *
+ * vocab 1 .. 2^31 - 1, dim 1 .. GCQ_LM_MAX_DIM, n <= GCQ_LM_MAX_ROWS.
+ * Errors: GCQ_ERR_PARAM (sizes, types, scale), GCQ_ERR_NULL, GCQ_ERR_ALIGN,
+ * GCQ_ERR_OVERLAP (out intersects an input), GCQ_ERR_LAUNCH.
+ */
+int embed_lookup(const void *table, int table_type, size_t vocab, size_t dim, size_t table_ld,
+                 const void *tokens, int token_type, size_t n, float scale, void *out,
+                 int out_type, size_t out_ld, void *stream);
+
+/*
+ * embed_sort -- orders n positions by token, for embed_grad and
+ * embed_grad_rows.  plan[0..n) receives the tokens in ascending order
+ * (padding last, as vocab), plan[n..2n) their positions, equal tokens in
+ * ascending position; the rest of the plan is scratch.
+ *
+ *   plan    out, uint32[embed_plan_words(n)], 4-byte aligned; belongs to this
+ *           n and vocab, and may be read by any number of calls
+ *
+ * Errors: GCQ_ERR_PARAM, GCQ_ERR_NULL, GCQ_ERR_ALIGN, GCQ_ERR_OVERLAP,
+ * GCQ_ERR_LAUNCH.
+ */
+int embed_sort(const void *tokens, int token_type, size_t n, size_t vocab, uint32_t *plan,
+               void *stream);
+
+/*
+ * embed_grad -- the gradient of embed_lookup in its table: for every v
+ *     d[v] = scale * (sum of grad[i] over the i with tokens[i] = v)
+ * in float32.  accumulate == 0: dtable = d, rows that no token names are
+ * zero.  Otherwise dtable += d, and rows that no token names are left as they
+ * are (gradients of several passes, or of a table tied to the output
+ * projection).  Positions of one token are summed in ascending order within
+ * runs of 32 sorted positions and the runs' sums in a fixed order.  Rows of
+ * grad at padding are not read.
+ *
+ *   grad    in,     n x dim of grad_type (a float type), rows grad_ld apart
+ *   plan    in,     from embed_sort with this n and vocab
+ *   dtable  in/out, float32, vocab x dim, rows dtable_ld apart
+ *   work    embed_work_bytes(n, dim) bytes, 16-byte aligned, contents not
+ *           kept; calls that may run at the same time need one each
+ *
+ * n == 0 without accumulate zeroes dtable.
+ * Errors: as embed_lookup.
+ */
+int embed_grad(const void *grad, int grad_type, size_t grad_ld, const uint32_t *plan, size_t n,
+               size_t vocab, size_t dim, float scale, int accumulate, float *dtable,
+               size_t dtable_ld, void *work, void *stream);
+
+/*
+ * embed_grad_rows -- the same gradient in row-sparse form, the exact message
+ * of a worker whose batch names few of the table's rows: the U different
+ * tokens in ascending order in ids[0..U), d of each in rows[0..U), U in
+ * *count.  Entries from U on are left as they were.  The messages of W
+ * workers, concatenated in worker order, are merged by embed_sort on their
+ * ids (entries past a worker's count set to -1) and embed_grad or
+ * embed_grad_rows on their rows: each token's rows are added in worker order.
+ *
+ *   ids     out, int32[min(n, vocab)], 4-byte aligned
+ *   rows    out, float32, min(n, vocab) x dim, rows rows_ld apart
+ *   count   out, int32
+ *
+ * n == 0 writes *count = 0.
+ * Errors: as embed_grad.
+ */
+int embed_grad_rows(const void *grad, int grad_type, size_t grad_ld, const uint32_t *plan,
+                    size_t n, size_t vocab, size_t dim, float scale, int32_t *ids, float *rows,
+                    size_t rows_ld, int32_t *count, void *work, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Sizes and status names (pure host functions, no device access)      */
 /* ------------------------------------------------------------------ */
 
@@ -440,6 +550,11 @@ size_t qsgd_elias_max_words(size_t n, uint32_t d);
 size_t saps_mask_words(size_t n);
 /* ceil(n/8192): SAPS tiles (saps_mask writes one more offset than this). */
 size_t saps_num_tiles(size_t n);
+/* Words of an embed_sort plan (0 for n above GCQ_LM_MAX_ROWS). */
+size_t embed_plan_words(size_t n);
+/* Bytes of embed_grad's and embed_grad_rows' workspace (0 for sizes out of
+ * range). */
+size_t embed_work_bytes(size_t n, size_t dim);
 /* Static, never-NULL name of a status code. */
 const char *gcq_status_string(int status);
 
