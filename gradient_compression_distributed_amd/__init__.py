@@ -27,6 +27,8 @@ __all__ = [
     "probe_stream", "probe_reduce",
     "embed_lookup", "embed_sort", "EmbedPlan", "embed_grad", "embed_grad_rows",
     "embed_plan_words", "embed_work_bytes",
+    "rms_norm", "rms_norm_q8", "rms_norm_grad", "rms_norm_work_bytes",
+    "distill_loss", "distill_grad", "distill_loss_grad",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -142,6 +144,25 @@ def load():
     lib.embed_plan_words.restype = sz
     lib.embed_work_bytes.argtypes = [sz, sz]
     lib.embed_work_bytes.restype = sz
+    lib.rms_norm.argtypes = [vp, i32, sz, sz, sz, vp, sz, vp, i32, f32, vp, sz, vp, sz, vp, vp]
+    lib.rms_norm.restype = i32
+    lib.rms_norm_q8.argtypes = [vp, i32, sz, sz, sz, vp, sz, vp, i32, f32, u32, vp, sz, vp, vp, sz,
+                                vp, vp]
+    lib.rms_norm_q8.restype = i32
+    lib.rms_norm_grad.argtypes = [vp, i32, sz, sz, sz, vp, sz, vp, i32, vp, vp, sz, vp, sz, vp, i32,
+                                  vp, vp]
+    lib.rms_norm_grad.restype = i32
+    lib.rms_norm_work_bytes.argtypes = [sz, sz, i32]
+    lib.rms_norm_work_bytes.restype = sz
+    lib.distill_loss.argtypes = [vp, i32, sz, sz, sz, vp, i32, sz, vp, i32, sz, u32, f32, vp, f32,
+                                 vp, vp, vp]
+    lib.distill_loss.restype = i32
+    lib.distill_grad.argtypes = [vp, i32, sz, sz, sz, vp, vp, i32, sz, vp, i32, sz, u32, f32, vp,
+                                 f32, vp, sz, vp]
+    lib.distill_grad.restype = i32
+    lib.distill_loss_grad.argtypes = [vp, i32, sz, sz, sz, vp, i32, sz, vp, i32, sz, u32, f32, vp,
+                                      f32, vp, vp, vp, sz, vp]
+    lib.distill_loss_grad.restype = i32
     _lib = lib
     return lib
 
@@ -734,3 +755,213 @@ def embed_grad_rows(grad, plan: EmbedPlan, scale: float = 1.0, ids=None, rows=No
           ld, plan.words.data_ptr(), plan.n, plan.vocab, dim, scale, ids.data_ptr(),
           rows.data_ptr(), rows_ld, count.data_ptr(), work.data_ptr())
     return ids, rows, count
+
+
+def rms_norm_work_bytes(rows: int, dim: int, dtype) -> int:
+    import torch
+
+    return int(load().rms_norm_work_bytes(rows, dim, _type_code(torch.empty(0, dtype=dtype), "dtype")))
+
+
+def _rms_args(x, weight, residual, h, rstd):
+    """The checks rms_norm and rms_norm_q8 share; (device, rows, dim, type,
+    arguments of x and the residual, arguments of the weight, h, its
+    arguments, rstd)."""
+    import torch
+
+    dev = _on(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    rows, dim = x.shape
+    kind = _type_code(x, "x")
+    res, res_ld, h_at, h_ld = None, 0, None, 0
+    ld = _matrix(x, "x", rows, dim, dev)
+    if residual is not None:
+        _type_code(residual, "residual", (kind,))
+        res, res_ld = residual.data_ptr(), _matrix(residual, "residual", rows, dim, dev)
+        if h is None:
+            h = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
+        _type_code(h, "h", (kind,))
+        h_at, h_ld = h.data_ptr(), _matrix(h, "h", rows, dim, dev)
+    elif h is not None:
+        raise ValueError("h is x itself without a residual")
+    _vector(weight, "weight", dim, dev)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        _vector(rstd, "rstd", rows, dev, torch.float32)
+    return (dev, rows, dim, kind, (x.data_ptr(), kind, rows, dim, ld, res, res_ld, weight.data_ptr(),
+                                   _type_code(weight, "weight", (kind, 0))),
+            x if residual is None else h, (h_at, h_ld, rstd.data_ptr()), rstd)
+
+
+def rms_norm(x, weight, eps: float, residual=None, y=None, h=None, rstd=None):
+    """Root-mean-square norm of x (+ residual), times weight: returns (y, h,
+    rstd).  h is the sum, rounded to x's type (x itself without a residual;
+    it may be given as the residual, which is then updated), rstd what
+    rms_norm_grad needs."""
+    import torch
+
+    lib = load()
+    dev, rows, dim, kind, args, h, tail, rstd = _rms_args(x, weight, residual, h, rstd)
+    if y is None:
+        y = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
+    y_ld = _matrix(y, "y", rows, dim, dev)
+    _type_code(y, "y", (kind,))
+    _call(lib.rms_norm, "rms_norm", dev, *args, eps, y.data_ptr(), y_ld, *tail)
+    return y, h, rstd
+
+
+def rms_norm_q8(x, weight, eps: float, group: int = 128, residual=None, codes=None, scales=None,
+                h=None, rstd=None):
+    """rms_norm with y as e4m3 codes (torch.float8_e4m3fn) and a float32 scale
+    per group of 32, 64 or 128 columns (group 0: per row): y is about code *
+    scale.  Returns (codes, scales [rows, groups], h, rstd)."""
+    import torch
+
+    lib = load()
+    dev, rows, dim, _, args, h, tail, rstd = _rms_args(x, weight, residual, h, rstd)
+    if group not in (0, 32, 64, 128):
+        raise ValueError(f"group must be 0, 32, 64 or 128 (got {group})")
+    parts = -(-dim // group) if group else 1
+    if codes is None:
+        codes = torch.empty((rows, dim), dtype=torch.float8_e4m3fn, device=x.device)
+    if scales is None:
+        scales = torch.empty((rows, parts), dtype=torch.float32, device=x.device)
+    codes_ld = _matrix(codes, "codes", rows, dim, dev)
+    if codes.dtype not in (torch.float8_e4m3fn, torch.uint8):
+        raise TypeError(f"codes must be float8_e4m3fn or uint8 (got {codes.dtype})")
+    _vector(scales, "scales", rows * parts, dev, torch.float32)
+    _call(lib.rms_norm_q8, "rms_norm_q8", dev, *args, eps, group, codes.data_ptr(), codes_ld,
+          scales.data_ptr(), *tail)
+    return codes, scales, h, rstd
+
+
+def rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, accumulate: bool = False,
+                  work=None):
+    """Gradients of rms_norm for dy (and dh, the gradient that reaches h
+    otherwise): returns (dx, dweight).  dx is the gradient of x and of the
+    residual; it may be given as dh.  dweight is float32; with ``accumulate``
+    it is added to."""
+    import torch
+
+    lib = load()
+    dev = _on(dy, "dy")
+    if dy.dim() != 2:
+        raise ValueError("dy must be a matrix")
+    rows, dim = dy.shape
+    kind = _type_code(dy, "dy")
+    ld = _matrix(dy, "dy", rows, dim, dev)
+    h_ld = _matrix(h, "h", rows, dim, dev)
+    _type_code(h, "h", (kind,))
+    _vector(weight, "weight", dim, dev)
+    _vector(rstd, "rstd", rows, dev, torch.float32)
+    dh_at, dh_ld = None, 0
+    if dh is not None:
+        _type_code(dh, "dh", (kind,))
+        dh_at, dh_ld = dh.data_ptr(), _matrix(dh, "dh", rows, dim, dev)
+    if dx is None:
+        dx = torch.empty((rows, dim), dtype=dy.dtype, device=dy.device)
+    dx_ld = _matrix(dx, "dx", rows, dim, dev)
+    _type_code(dx, "dx", (kind,))
+    if dweight is None:
+        if accumulate:
+            raise ValueError("accumulate needs dweight")
+        dweight = torch.empty(dim, dtype=torch.float32, device=dy.device)
+    _vector(dweight, "dweight", dim, dev, torch.float32)
+    need = lib.rms_norm_work_bytes(rows, dim, kind)
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device=dy.device)
+    else:
+        _vector(work, "work", need, dev, torch.uint8, at_least=True)
+    _call(lib.rms_norm_grad, "rms_norm_grad", dev, dy.data_ptr(), kind, rows, dim, ld, h.data_ptr(),
+          h_ld, weight.data_ptr(), _type_code(weight, "weight", (kind, 0)), rstd.data_ptr(), dh_at,
+          dh_ld, dx.data_ptr(), dx_ld, dweight.data_ptr(), accumulate, work.data_ptr())
+    return dx, dweight
+
+
+def _distill_args(logits, index, teacher, temperature, row_scale, scale):
+    """The checks the three calls share; (device, rows, vocab, type, the
+    logits' arguments, the arguments behind them)."""
+    dev = _on(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be a matrix")
+    rows, vocab = logits.shape
+    kind = _type_code(logits, "logits")
+    ld = _matrix(logits, "logits", rows, vocab, dev)
+    k = index.shape[-1] if index.dim() else 0
+    idx_ld = _matrix(index, "index", rows, k, dev)
+    top_ld = _matrix(teacher, "teacher", rows, k, dev)
+    if row_scale is not None:
+        import torch
+
+        _vector(row_scale, "row_scale", rows, dev, torch.float32)
+    return (dev, rows, vocab, kind, (logits.data_ptr(), kind, rows, vocab, ld),
+            (index.data_ptr(), _type_code(index, "index", (3, 4)), idx_ld, teacher.data_ptr(),
+             _type_code(teacher, "teacher", (kind, 0)), top_ld, k, temperature,
+             None if row_scale is None else row_scale.data_ptr(), scale))
+
+
+def _row_floats(x, name, rows, dev, like):
+    """A float32 vector of a value per row, new if none is given."""
+    import torch
+
+    if x is None:
+        return torch.empty(rows, dtype=torch.float32, device=like.device)
+    _vector(x, name, rows, dev, torch.float32)
+    return x
+
+
+def _dlogits(out, logits, rows, vocab, kind, dev):
+    import torch
+
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    _type_code(out, "out", (kind,))
+    return out, _matrix(out, "out", rows, vocab, dev)
+
+
+def distill_loss(logits, index, teacher, temperature: float = 1.0, row_scale=None,
+                 scale: float = 1.0, loss=None, lse=None):
+    """Distillation from a teacher's top logits: returns (loss, lse), float32
+    per row.  ``index`` and ``teacher`` are [rows, k]: the teacher's entries
+    and their logits (an index outside the vocabulary marks an absent one).
+    loss = s * KL(softmax(teacher / T) || softmax(logits / T)), the student's
+    softmax over the whole vocabulary, s = scale * row_scale; rows with s = 0
+    are not read."""
+    lib = load()
+    dev, rows, _, _, head, tail = _distill_args(logits, index, teacher, temperature, row_scale, scale)
+    loss = _row_floats(loss, "loss", rows, dev, logits)
+    lse = _row_floats(lse, "lse", rows, dev, logits)
+    _call(lib.distill_loss, "distill_loss", dev, *head, *tail, loss.data_ptr(), lse.data_ptr())
+    return loss, lse
+
+
+def distill_grad(logits, lse, index, teacher, temperature: float = 1.0, row_scale=None,
+                 scale: float = 1.0, out=None):
+    """The gradient of sum(loss) in the logits, from distill_loss's lse;
+    ``row_scale`` may carry the gradient from above.  out may be the logits."""
+    import torch
+
+    lib = load()
+    dev, rows, vocab, kind, head, tail = _distill_args(logits, index, teacher, temperature, row_scale,
+                                                       scale)
+    _vector(lse, "lse", rows, dev, torch.float32)
+    out, ld = _dlogits(out, logits, rows, vocab, kind, dev)
+    _call(lib.distill_grad, "distill_grad", dev, *head, lse.data_ptr(), *tail, out.data_ptr(), ld)
+    return out
+
+
+def distill_loss_grad(logits, index, teacher, temperature: float = 1.0, row_scale=None,
+                      scale: float = 1.0, loss=None, lse=None, out=None):
+    """distill_loss and distill_grad in one launch: (loss, lse, dlogits).  out
+    may be the logits, which it then replaces."""
+    lib = load()
+    dev, rows, vocab, kind, head, tail = _distill_args(logits, index, teacher, temperature, row_scale,
+                                                       scale)
+    loss = _row_floats(loss, "loss", rows, dev, logits)
+    lse = _row_floats(lse, "lse", rows, dev, logits)
+    out, ld = _dlogits(out, logits, rows, vocab, kind, dev)
+    _call(lib.distill_loss_grad, "distill_loss_grad", dev, *head, *tail, loss.data_ptr(),
+          lse.data_ptr(), out.data_ptr(), ld)
+    return loss, lse, out

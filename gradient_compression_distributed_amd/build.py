@@ -14,7 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libgcq.so")
 SOURCES = [os.path.join(CSRC, f) for f in
            ("gc2_quantize.hip", "dequant_reduce.hip", "qsgd.hip", "saps.hip", "elias.hip", "probe.hip", "gcq_runtime.hip",
-            "gcq_api.hip", "embed.hip", "gcq_api_lm.hip")]
+            "gcq_api.hip", "embed.hip", "rms_norm.hip", "distill.hip", "gcq_api_lm.hip")]
 ARCH = os.environ.get("GCQ_OFFLOAD_ARCH", "gfx950")
 
 HIPFLAGS = [

@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(const T *__restrict__
 {
     constexpr int N = kVec<T>;
     const uint32_t lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes;
-    const uint64_t row = (uint64_t)blockIdx.x * (256u / lanes) + slot;
+    const uint64_t row = block_number() * (256u / lanes) + slot;
     if (row >= n)
         return;
     const uint64_t tok = (uint64_t)(int64_t)((const GCQ_G I *)tokens)[row];
@@ -504,7 +504,7 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, u
 __global__ __launch_bounds__(256) void embed_zero_kernel(EmbedGrad e)
 {
     __shared__ uint64_t untouched;
-    const uint64_t v0 = (uint64_t)blockIdx.x * kWave;
+    const uint64_t v0 = block_number() * kWave;
     if (threadIdx.x < kWave) {
         const uint64_t v = v0 + threadIdx.x;
         uint64_t lo = 0, hi = e.n;
@@ -542,10 +542,8 @@ hipError_t lookup(const EmbedTable &t, const void *tokens, uint64_t n, float sca
                   uint64_t out_ld, hipStream_t s)
 {
     const uint32_t lanes = lanes_for(t.dim, kVec<T>);
-    const uint64_t per = 256u / lanes, grid = (n + per - 1) / per;
-    if (grid > 0x7FFFFFFFu)
-        return hipErrorInvalidValue;
-    embed_lookup_kernel<T, O, I><<<(uint32_t)grid, 256, 0, s>>>(
+    const uint64_t per = 256u / lanes;
+    embed_lookup_kernel<T, O, I><<<block_grid((n + per - 1) / per), 256, 0, s>>>(
         (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
     return hipGetLastError();
 }
@@ -619,7 +617,7 @@ hipError_t grad(const EmbedGrad &e, hipStream_t s)
     if (F == Form::kRows && !runs)
         embed_scan_kernel<<<1, kScanThreads, 0, s>>>((uint32_t *)e.count, 0, true);
     if constexpr (F == Form::kWrite)
-        embed_zero_kernel<<<(uint32_t)((e.vocab + kWave - 1) / kWave), 256, 0, s>>>(e);
+        embed_zero_kernel<<<block_grid((e.vocab + kWave - 1) / kWave), 256, 0, s>>>(e);
     if (!runs)
         return hipGetLastError();
     if constexpr (F == Form::kRows) {
@@ -631,8 +629,6 @@ hipError_t grad(const EmbedGrad &e, hipStream_t s)
     const int vec = e.type == GCQ_F32 ? kVec<float> : kVec<_Float16>;
     const uint32_t lanes = lanes_for(e.dim, vec), groups = 256u / lanes;
     const uint64_t cols = (e.dim + (uint64_t)lanes * vec - 1) / ((uint64_t)lanes * vec);
-    if (cols > 65535)
-        return hipErrorInvalidValue;
     const dim3 grid((uint32_t)((runs + groups - 1) / groups), (uint32_t)cols);
     switch (e.type) {
     case GCQ_F32: embed_grad_kernel<float, F><<<grid, 256, 0, s>>>(e, lanes); break;

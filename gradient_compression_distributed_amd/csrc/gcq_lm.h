@@ -85,6 +85,19 @@ __device__ __forceinline__ float max_lanes(float x)
     return x;
 }
 
+// A launch's workgroups in two dimensions (one dimension holds at most 2^32
+// threads), and the workgroup's number among them.
+inline dim3 block_grid(uint64_t blocks)
+{
+    const uint32_t x = blocks < 65536u ? (uint32_t)blocks : 65536u;
+    return dim3(x, (uint32_t)((blocks + x - 1) / x));
+}
+
+__device__ __forceinline__ uint64_t block_number()
+{
+    return (uint64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
 }  // namespace lm
 
 // ---- embedding ----------------------------------------------------------
@@ -126,5 +139,54 @@ hipError_t launch_embed_lookup(const EmbedTable &t, const void *tokens, bool tok
 hipError_t launch_embed_sort(const void *tokens, bool tok64, uint64_t n, uint64_t vocab,
                              uint32_t *plan, hipStream_t stream);
 hipError_t launch_embed_grad(const EmbedGrad &e, hipStream_t stream);
+
+// ---- root-mean-square norm ------------------------------------------------
+struct RmsNorm {
+    int type;
+    bool w_f32;                     // w is float32 (else of `type`)
+    const void *x, *res, *w;        // res may be null
+    uint64_t rows, dim, x_ld, res_ld, y_ld, h_ld;
+    float eps;
+    void *y;                        // plain output
+    uint8_t *codes;                 // or e4m3 codes (rows y_ld apart) and scales
+    float *scales;
+    uint32_t group;                 // columns per scale; 0: the whole row
+    uint64_t parts;                 // scales per row
+    void *h;                        // may be null
+    float *rstd;                    // may be null
+};
+
+struct RmsGrad {
+    int type;
+    bool w_f32;
+    const void *dy, *h, *w, *dh;    // dh may be null
+    const float *rstd;
+    uint64_t rows, dim, dy_ld, h_ld, dh_ld, dx_ld;
+    void *dx;
+    float *dw;
+    bool add;                       // dw is added to
+    float *part_w;                  // workspace: [slots][dim]
+    uint64_t slots;
+};
+
+uint64_t rms_norm_work_bytes(uint64_t rows, uint64_t dim, int type);
+hipError_t launch_rms_norm(const RmsNorm &a, hipStream_t stream);
+hipError_t launch_rms_norm_grad(const RmsGrad &a, hipStream_t stream);
+
+// ---- distillation from top logits -----------------------------------------
+struct Distill {
+    int type;                       // of z, dz and (unless t_f32) the teacher's logits
+    bool t_f32, idx64;
+    const void *z, *idx, *top;
+    uint64_t rows, vocab, z_ld, idx_ld, top_ld, dz_ld;
+    uint32_t k;
+    float temp, scale;
+    const float *row_scale;         // may be null
+    const float *lse;               // null: the loss is wanted; else dz from it
+    float *loss, *lse_out;
+    void *dz;                       // with the loss: may be null
+};
+
+hipError_t launch_distill(const Distill &a, hipStream_t stream);
 
 }  // namespace gcq

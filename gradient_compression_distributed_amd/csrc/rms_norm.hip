@@ -1,0 +1,517 @@
+// rms_norm.hip -- root-mean-square norm with the residual's addition, its
+// output plain or in 8 bits with scales, and its gradient, for gfx950.
+//
+//   h = x + residual          (x alone without a residual)
+//   rstd = 1 / sqrt(mean(h^2) + eps)
+//   y = h * rstd * w
+//   8 bits, per group of columns: a = max |y|,
+//     scale = 0 if a = 0, else max(a / 448, 2^-126);  code = e4m3(y / scale)
+// and for an output gradient dy (the 8-bit rounding passes it straight on)
+// and the gradient dh that reaches h by other ways:
+//   u = dy * w;  dx = rstd * (u - h * rstd^2 * mean(u * h)) + dh
+//   dw = sum over rows of dy * h * rstd
+//
+// A row stays in the registers of the lanes that share it between the pass
+// for its statistics and the pass that uses them, so every matrix is read
+// once.  Statistics are taken from h before it is rounded for storing.
+#include "gcq_device.h"
+#include "gcq_lm.h"
+
+namespace gcq {
+
+namespace {
+
+using namespace lm;
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kMinNormal = 1.17549435e-38f;   // 2^-126: its reciprocal is finite
+
+// Sum (or maximum) over the L lanes of a row; for L > 64 the workgroup is
+// one row and `part` holds a value per wavefront.  The caller alternates
+// between two parts, so one barrier per reduction is enough.
+template <int L, bool Max>
+__device__ __forceinline__ float row_reduce(float x, float *part)
+{
+    x = Max ? max_lanes(x) : sum_lanes(x);
+    if constexpr (L > kWave) {
+        if ((threadIdx.x & (kWave - 1)) == 0)
+            part[threadIdx.x / kWave] = x;
+        __syncthreads();
+        x = part[0];
+#pragma unroll
+        for (int w = 1; w < L / kWave; ++w)
+            x = Max ? fmaxf(x, part[w]) : x + part[w];
+    }
+    return x;
+}
+
+template <int N>
+__device__ __forceinline__ fvec<N> load_weight(const void *w, bool f32, uint64_t c, int64_t left,
+                                               const float *)
+{
+    return load_vec<float, N>((const float *)w + c, left);
+}
+
+template <int N, typename T>
+__device__ __forceinline__ fvec<N> load_weight(const void *w, bool f32, uint64_t c, int64_t left,
+                                               const T *)
+{
+    if (f32)
+        return load_vec<float, N>((const float *)w + c, left);
+    return to_f32<T, N>(load_vec<T, N>((const T *)w + c, left));
+}
+
+// Two e4m3 codes per conversion, four per word, lowest byte first.
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t *p, fvec<N> v, int64_t left)
+{
+    uint32_t q[N / 4];
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        int word = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i], v[4 * i + 1], 0, false);
+        q[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * i + 2], v[4 * i + 3], word, true);
+    }
+    vec<uint8_t, N> b;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        b[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+    store_vec<uint8_t, N>(p, b, left);
+}
+
+// Scale of a group whose largest magnitude is a, and the factor that takes
+// values to codes (one division per group; the factor's rounding can move a
+// value within 2^-23 of a tie to its other neighbour).
+__device__ __forceinline__ float group_scale(float a, float &inv)
+{
+    const float s = a == 0.0f ? 0.0f : fmaxf(a / kE4m3Max, kMinNormal);
+    inv = s == 0.0f ? 0.0f : 1.0f / s;
+    return s;
+}
+
+// A row's lanes hold Ch vectors of N columns, L * N columns apart.
+template <typename T, int L, int Ch, bool Q8>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_kernel(RmsNorm a)
+{
+    constexpr int N = kVec<T>, Threads = L < 256 ? 256 : L;
+    __shared__ float part[2][Threads / kWave];
+    const uint32_t lane = threadIdx.x & (L - 1);
+    const uint64_t row = block_number() * (Threads / L) + threadIdx.x / L;
+    if (row >= a.rows)
+        return;   // a whole workgroup, or a wavefront of one without barriers
+    const T *x = (const T *)a.x + row * a.x_ld, *res = (const T *)a.res + row * a.res_ld;
+    fvec<N> h[Ch];
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Ch; ++i) {
+        const uint64_t c = ((uint64_t)i * L + lane) * N;
+        h[i] = 0.0f;
+        if (c < a.dim) {
+            const int64_t left = (int64_t)(a.dim - c);
+            h[i] = to_f32<T, N>(load_vec<T, N>(x + c, left));
+            if (a.res)
+                h[i] += to_f32<T, N>(load_vec<T, N>(res + c, left));
+            if (a.h)
+                store_vec<T, N>((T *)a.h + row * a.h_ld + c, from_f32<T, N>(h[i]), left);
+        }
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            sum = fmaf(h[i][j], h[i][j], sum);
+    }
+    sum = row_reduce<L, false>(sum, part[0]);
+    const float rstd = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
+    if (a.rstd && lane == 0)
+        a.rstd[row] = rstd;
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < Ch; ++i) {
+        const uint64_t c = ((uint64_t)i * L + lane) * N;
+        if (c < a.dim) {
+            const int64_t left = (int64_t)(a.dim - c);
+            h[i] = h[i] * rstd * load_weight<N>(a.w, a.w_f32, c, left, x);
+            if constexpr (!Q8)
+                store_vec<T, N>((T *)a.y + row * a.y_ld + c, from_f32<T, N>(h[i]), left);
+        }
+        if constexpr (Q8) {
+            float m = 0.0f;
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                m = fmaxf(m, fabsf(h[i][j]));
+            top = fmaxf(top, m);
+            if (a.group) {   // a group is the columns of group / N neighbouring lanes
+                for (uint32_t o = 1; o * N < a.group; o <<= 1)
+                    m = fmaxf(m, __shfl_xor(m, (int)o, kWave));
+                float inv;
+                const float s = group_scale(m, inv);
+                if (c < a.dim) {
+                    if (c % a.group == 0)
+                        a.scales[row * a.parts + c / a.group] = s;
+                    store_codes<N>(a.codes + row * a.y_ld + c, h[i] * inv, (int64_t)(a.dim - c));
+                }
+            }
+        }
+    }
+    if constexpr (Q8) {
+        if (!a.group) {
+            float inv;
+            const float s = group_scale(row_reduce<L, true>(top, part[1]), inv);
+            if (lane == 0)
+                a.scales[row] = s;
+#pragma unroll
+            for (int i = 0; i < Ch; ++i) {
+                const uint64_t c = ((uint64_t)i * L + lane) * N;
+                if (c < a.dim)
+                    store_codes<N>(a.codes + row * a.y_ld + c, h[i] * inv, (int64_t)(a.dim - c));
+            }
+        }
+    }
+}
+
+// Rows too long for the registers of a workgroup: the row is read again for
+// each pass (from the caches).  h is written by the last pass, so it may take
+// the residual's or x's place.
+template <typename T, bool Q8>
+__global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNorm a)
+{
+    constexpr int N = kVec<T>, L = 1024;
+    __shared__ float part[2][L / kWave];
+    const uint64_t row = block_number();
+    if (row >= a.rows)
+        return;
+    const T *x = (const T *)a.x + row * a.x_ld, *res = (const T *)a.res + row * a.res_ld;
+    auto load_h = [&](uint64_t c, int64_t left) {
+        fvec<N> h = to_f32<T, N>(load_vec<T, N>(x + c, left));
+        if (a.res)
+            h += to_f32<T, N>(load_vec<T, N>(res + c, left));
+        return h;
+    };
+    const uint64_t step = (uint64_t)L * N, c0 = (uint64_t)threadIdx.x * N;
+    float sum = 0.0f;
+    for (uint64_t c = c0; c < a.dim; c += step) {
+        const fvec<N> h = load_h(c, (int64_t)(a.dim - c));
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            sum = fmaf(h[j], h[j], sum);
+    }
+    sum = row_reduce<L, false>(sum, part[0]);
+    const float rstd = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
+    if (a.rstd && threadIdx.x == 0)
+        a.rstd[row] = rstd;
+    float inv = 0.0f;
+    if constexpr (Q8) {
+        if (!a.group) {
+            float top = 0.0f;
+            for (uint64_t c = c0; c < a.dim; c += step) {
+                const int64_t left = (int64_t)(a.dim - c);
+                const fvec<N> y = load_h(c, left) * rstd * load_weight<N>(a.w, a.w_f32, c, left, x);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    top = fmaxf(top, fabsf(y[j]));
+            }
+            const float s = group_scale(row_reduce<L, true>(top, part[1]), inv);
+            if (threadIdx.x == 0)
+                a.scales[row] = s;
+        }
+    }
+    // every lane takes part in a group's maximum: whole steps
+    for (uint64_t b = 0; b < a.dim; b += step) {
+        const uint64_t c = b + c0;
+        const int64_t left = (int64_t)a.dim - (int64_t)c;
+        fvec<N> y = 0.0f;
+        if (left > 0) {
+            const fvec<N> h = load_h(c, left);
+            y = h * rstd * load_weight<N>(a.w, a.w_f32, c, left, x);
+            if (a.h)
+                store_vec<T, N>((T *)a.h + row * a.h_ld + c, from_f32<T, N>(h), left);
+            if constexpr (!Q8)
+                store_vec<T, N>((T *)a.y + row * a.y_ld + c, from_f32<T, N>(y), left);
+        }
+        if constexpr (Q8) {
+            if (a.group) {
+                float m = 0.0f;
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    m = fmaxf(m, fabsf(y[j]));
+                for (uint32_t o = 1; o * N < a.group; o <<= 1)
+                    m = fmaxf(m, __shfl_xor(m, (int)o, kWave));
+                const float s = group_scale(m, inv);
+                if (left > 0 && c % a.group == 0)
+                    a.scales[row * a.parts + c / a.group] = s;
+            }
+            if (left > 0)
+                store_codes<N>(a.codes + row * a.y_ld + c, y * inv, left);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// A slot is the L lanes that share a row; slot s takes rows s, s + slots, ...
+// and keeps its share of dw in registers, written to part_w[s] at the end.
+template <typename T, int L, int Ch>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_grad_kernel(RmsGrad a)
+{
+    constexpr int N = kVec<T>, Threads = L < 256 ? 256 : L;
+    __shared__ float part[2][Threads / kWave];
+    const uint32_t lane = threadIdx.x & (L - 1);
+    const uint64_t slot = (uint64_t)blockIdx.x * (Threads / L) + threadIdx.x / L;
+    if (slot >= a.slots)
+        return;   // only where a workgroup holds several slots: no barriers then
+    fvec<N> dw[Ch];
+#pragma unroll
+    for (int i = 0; i < Ch; ++i)
+        dw[i] = 0.0f;
+    uint32_t turn = 0;
+    for (uint64_t row = slot; row < a.rows; row += a.slots, turn ^= 1u) {
+        const T *dy = (const T *)a.dy + row * a.dy_ld, *h = (const T *)a.h + row * a.h_ld;
+        const T *dh = (const T *)a.dh + row * a.dh_ld;
+        vec<T, N> gv[Ch], hv[Ch], dv[Ch];
+        const float rstd = a.rstd[row];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < Ch; ++i) {
+            const uint64_t c = ((uint64_t)i * L + lane) * N;
+            gv[i] = hv[i] = dv[i] = (T)0.0f;
+            if (c < a.dim) {
+                const int64_t left = (int64_t)(a.dim - c);
+                gv[i] = load_vec<T, N>(dy + c, left);
+                hv[i] = load_vec<T, N>(h + c, left);
+                if (a.dh)
+                    dv[i] = load_vec<T, N>(dh + c, left);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < Ch; ++i) {
+            const uint64_t c = ((uint64_t)i * L + lane) * N;
+            fvec<N> w = 0.0f;
+            if (c < a.dim)
+                w = load_weight<N>(a.w, a.w_f32, c, (int64_t)(a.dim - c), dy);
+            const fvec<N> g = to_f32<T, N>(gv[i]), hf = to_f32<T, N>(hv[i]);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                sum = fmaf(g[j] * w[j], hf[j], sum);
+                dw[i][j] = fmaf(g[j], hf[j] * rstd, dw[i][j]);
+            }
+        }
+        sum = row_reduce<L, false>(sum, part[turn]);
+        const float k = sum / (float)a.dim * rstd * rstd;
+#pragma unroll
+        for (int i = 0; i < Ch; ++i) {
+            const uint64_t c = ((uint64_t)i * L + lane) * N;
+            if (c >= a.dim)
+                continue;
+            const int64_t left = (int64_t)(a.dim - c);
+            const fvec<N> w = load_weight<N>(a.w, a.w_f32, c, left, dy);
+            const fvec<N> g = to_f32<T, N>(gv[i]), hf = to_f32<T, N>(hv[i]);
+            fvec<N> d = to_f32<T, N>(dv[i]);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                d[j] = fmaf(rstd, fmaf(-hf[j], k, g[j] * w[j]), d[j]);
+            store_vec<T, N>((T *)a.dx + row * a.dx_ld + c, from_f32<T, N>(d), left);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < Ch; ++i) {
+        const uint64_t c = ((uint64_t)i * L + lane) * N;
+        if (c < a.dim)
+            store_vec<float, N>(a.part_w + slot * a.dim + c, dw[i], (int64_t)(a.dim - c));
+    }
+}
+
+// Long rows: read twice; the slot's share of dw lives in its workspace row
+// (each element is always the same lane's).
+template <typename T>
+__global__ __launch_bounds__(1024) void rms_norm_grad_long_kernel(RmsGrad a)
+{
+    constexpr int N = kVec<T>, L = 1024;
+    __shared__ float part[2][L / kWave];
+    const uint64_t slot = blockIdx.x, step = (uint64_t)L * N, c0 = (uint64_t)threadIdx.x * N;
+    float *pw = a.part_w + slot * a.dim;
+    uint32_t turn = 0;
+    for (uint64_t row = slot; row < a.rows; row += a.slots, turn ^= 1u) {
+        const T *dy = (const T *)a.dy + row * a.dy_ld, *h = (const T *)a.h + row * a.h_ld;
+        const T *dh = (const T *)a.dh + row * a.dh_ld;
+        const float rstd = a.rstd[row];
+        float sum = 0.0f;
+        for (uint64_t c = c0; c < a.dim; c += step) {
+            const int64_t left = (int64_t)(a.dim - c);
+            const fvec<N> g = to_f32<T, N>(load_vec<T, N>(dy + c, left));
+            const fvec<N> hf = to_f32<T, N>(load_vec<T, N>(h + c, left));
+            const fvec<N> w = load_weight<N>(a.w, a.w_f32, c, left, dy);
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                sum = fmaf(g[j] * w[j], hf[j], sum);
+        }
+        sum = row_reduce<L, false>(sum, part[turn]);
+        const float k = sum / (float)a.dim * rstd * rstd;
+        for (uint64_t c = c0; c < a.dim; c += step) {
+            const int64_t left = (int64_t)(a.dim - c);
+            const fvec<N> g = to_f32<T, N>(load_vec<T, N>(dy + c, left));
+            const fvec<N> hf = to_f32<T, N>(load_vec<T, N>(h + c, left));
+            const fvec<N> w = load_weight<N>(a.w, a.w_f32, c, left, dy);
+            fvec<N> d = 0.0f, dw = 0.0f;
+            if (a.dh)
+                d = to_f32<T, N>(load_vec<T, N>(dh + c, left));
+            if (row != slot)
+                dw = load_vec<float, N>(pw + c, left);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                d[j] = fmaf(rstd, fmaf(-hf[j], k, g[j] * w[j]), d[j]);
+                dw[j] = fmaf(g[j], hf[j] * rstd, dw[j]);
+            }
+            store_vec<T, N>((T *)a.dx + row * a.dx_ld + c, from_f32<T, N>(d), left);
+            store_vec<float, N>(pw + c, dw, left);
+        }
+    }
+}
+
+// dw[c] (+)= the slots' shares, by 16 wavefronts over every 16th slot and
+// their sums in order; a lane per column.
+constexpr uint32_t kDwThreads = 1024;
+__global__ __launch_bounds__(kDwThreads) void rms_norm_dw_kernel(const float *__restrict__ part_w,
+                                                                 uint64_t slots, uint64_t dim,
+                                                                 float *__restrict__ dw, bool add)
+{
+    constexpr uint32_t waves = kDwThreads / kWave;
+    __shared__ float share[waves][kWave];
+    const uint32_t lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const uint64_t c = (uint64_t)blockIdx.x * kWave + lane;
+    float sum = 0.0f;
+    if (c < dim) {
+#pragma unroll 8
+        for (uint64_t s = wave; s < slots; s += waves)
+            sum += part_w[s * dim + c];
+    }
+    share[wave][lane] = sum;
+    __syncthreads();
+    if (wave == 0 && c < dim) {
+        for (uint32_t w = 1; w < waves; ++w)
+            sum += share[w][lane];
+        dw[c] = add ? dw[c] + sum : sum;
+    }
+}
+
+// Lanes per row and vectors per lane (0: too long for registers).  64 and
+// 256 lanes take up to `most` vectors each; 1024 lanes hold 32 float32 or 16
+// 16-bit elements each before they spill.
+struct Split {
+    int lanes, ch;
+};
+
+template <typename T>
+Split split_row(uint64_t dim, uint64_t most)
+{
+    const uint64_t vecs = (dim + kVec<T> - 1) / kVec<T>;
+    for (int lanes : {64, 256})
+        if (vecs <= lanes * most)
+            return {lanes, vecs <= (uint64_t)lanes ? 1 : 2};
+    return {1024, vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 && sizeof(T) == 4 ? 4 : 0};
+}
+
+template <typename T, int L, int Ch>
+void norm(const RmsNorm &a, hipStream_t s)
+{
+    constexpr int threads = L < 256 ? 256 : L, per = threads / L;
+    const dim3 grid = block_grid((a.rows + per - 1) / per);
+    if (a.codes)
+        rms_norm_kernel<T, L, Ch, true><<<grid, threads, 0, s>>>(a);
+    else
+        rms_norm_kernel<T, L, Ch, false><<<grid, threads, 0, s>>>(a);
+}
+
+template <typename T, int L>
+void norm(const RmsNorm &a, int ch, hipStream_t s)
+{
+    if (ch == 1)
+        norm<T, L, 1>(a, s);
+    else if (ch == 2)
+        norm<T, L, 2>(a, s);
+    else if constexpr (L == 1024 && sizeof(T) == 4)
+        norm<T, L, 4>(a, s);
+}
+
+template <typename T>
+void norm(const RmsNorm &a, hipStream_t s)
+{
+    const Split p = split_row<T>(a.dim, a.rows >= 1024 ? 2 : 1);
+    if (!p.ch) {
+        if (a.codes)
+            rms_norm_long_kernel<T, true><<<block_grid(a.rows), 1024, 0, s>>>(a);
+        else
+            rms_norm_long_kernel<T, false><<<block_grid(a.rows), 1024, 0, s>>>(a);
+    } else if (p.lanes == 64) {
+        norm<T, 64>(a, p.ch, s);
+    } else if (p.lanes == 256) {
+        norm<T, 256>(a, p.ch, s);
+    } else {
+        norm<T, 1024>(a, p.ch, s);
+    }
+}
+
+// Slots of the gradient: enough rows in flight to fill the device, few
+// enough that their shares of dw are a small part of the traffic.
+uint64_t grad_slots(uint64_t rows, int lanes)
+{
+    const uint64_t most = lanes == 64 ? 2048 : lanes == 256 ? 1024 : 512;
+    return rows < most ? rows : most;
+}
+
+template <typename T, int L>
+void norm_grad(const RmsGrad &a, int ch, hipStream_t s)
+{
+    constexpr int threads = L < 256 ? 256 : L, per = threads / L;
+    const uint32_t grid = (uint32_t)((a.slots + per - 1) / per);
+    if (ch == 1)
+        rms_norm_grad_kernel<T, L, 1><<<grid, threads, 0, s>>>(a);
+    else if (ch == 2)
+        rms_norm_grad_kernel<T, L, 2><<<grid, threads, 0, s>>>(a);
+    else if constexpr (L == 1024 && sizeof(T) == 4)
+        rms_norm_grad_kernel<T, L, 4><<<grid, threads, 0, s>>>(a);
+}
+
+template <typename T>
+hipError_t norm_grad(RmsGrad a, hipStream_t s)
+{
+    const Split p = split_row<T>(a.dim, 2);
+    a.slots = grad_slots(a.rows, p.lanes);
+    if (a.rows) {
+        if (!p.ch)
+            rms_norm_grad_long_kernel<T><<<(uint32_t)a.slots, 1024, 0, s>>>(a);
+        else if (p.lanes == 64)
+            norm_grad<T, 64>(a, p.ch, s);
+        else if (p.lanes == 256)
+            norm_grad<T, 256>(a, p.ch, s);
+        else
+            norm_grad<T, 1024>(a, p.ch, s);
+    }
+    rms_norm_dw_kernel<<<(uint32_t)((a.dim + kWave - 1) / kWave), kDwThreads, 0, s>>>(
+        a.part_w, a.slots, a.dim, a.dw, a.add);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+uint64_t rms_norm_work_bytes(uint64_t rows, uint64_t dim, int type)
+{
+    const Split p = type == GCQ_F32 ? split_row<float>(dim, 2) : split_row<_Float16>(dim, 2);
+    return 4 * dim * grad_slots(rows, p.lanes);
+}
+
+hipError_t launch_rms_norm(const RmsNorm &a, hipStream_t stream)
+{
+    switch (a.type) {
+    case GCQ_F32: norm<float>(a, stream); break;
+    case GCQ_F16: norm<_Float16>(a, stream); break;
+    default: norm<__bf16>(a, stream); break;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_grad(const RmsGrad &a, hipStream_t stream)
+{
+    switch (a.type) {
+    case GCQ_F32: return norm_grad<float>(a, stream);
+    case GCQ_F16: return norm_grad<_Float16>(a, stream);
+    default: return norm_grad<__bf16>(a, stream);
+    }
+}
+
+}  // namespace gcq

@@ -446,7 +446,7 @@ enum gcq_type {
 };
 
 /* Largest row (token) count and row length of the operators below. */
-#define GCQ_LM_MAX_ROWS ((size_t)1 << 30)
+#define GCQ_LM_MAX_ROWS ((size_t)1 << 24)
 #define GCQ_LM_MAX_DIM ((size_t)1 << 22)
 
 /* ------------------------------------------------------------------ */
@@ -530,6 +530,135 @@ int embed_grad_rows(const void *grad, int grad_type, size_t grad_ld, const uint3
                     size_t rows_ld, int32_t *count, void *work, void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Root-mean-square norm, plain or to 8 bits, and its gradient         */
+/* ------------------------------------------------------------------ */
+
+/*
+ * rms_norm -- for every row, in float32:
+ *     h = x + residual     (h = x without a residual)
+ *     rstd = 1 / sqrt(mean(h^2) + eps)
+ *     y = h * rstd * weight
+ * The statistics are taken from h before it is rounded for storing.
+ *
+ *   x         in,  rows x dim of `type` (a float type), rows x_ld apart
+ *   residual  in,  like x, or NULL
+ *   weight    in,  dim of weight_type: `type` or GCQ_F32
+ *   eps       finite and >= 0
+ *   y         out, rows x dim of `type`
+ *   h         out, rows x dim of `type` (the residual stream's next value),
+ *             or NULL; needs a residual.  It may be x or the residual itself
+ *             (same address and ld)
+ *   rstd      out, float32[rows], or NULL (rms_norm_grad needs it)
+ *
+ * dim 1 .. GCQ_LM_MAX_DIM, rows <= GCQ_LM_MAX_ROWS.  A NaN or an infinity in
+ * a row follows IEEE arithmetic through its mean.
+ * Errors: GCQ_ERR_PARAM, GCQ_ERR_NULL, GCQ_ERR_ALIGN, GCQ_ERR_OVERLAP,
+ * GCQ_ERR_LAUNCH.
+ */
+int rms_norm(const void *x, int type, size_t rows, size_t dim, size_t x_ld, const void *residual,
+             size_t residual_ld, const void *weight, int weight_type, float eps, void *y,
+             size_t y_ld, void *h, size_t h_ld, float *rstd, void *stream);
+
+/*
+ * rms_norm_q8 -- rms_norm with y in 8 bits, scaled by its largest magnitude
+ * per group of `group` consecutive columns (the last group of a row may be
+ * shorter), as qsgd_quantize_maxnorm scales its buckets:
+ *     a = max |y| over the group, a NaN never becoming the maximum
+ *     scale = 0 if a = 0, else max(a / 448, 2^-126)
+ *     code = y * (1 / scale) to the nearest OCP e4m3 value, ties to even
+ *            (0 where scale = 0, NaN for a NaN)
+ * so y is about scale * code.  Nothing overflows: 448 is e4m3's largest.
+ *
+ *   group   32, 64 or 128; 0: the whole row
+ *   codes   out, rows x dim bytes, rows codes_ld apart
+ *   scales  out, float32[rows][ceil(dim / group)] ([rows] for group 0)
+ *
+ * Others and errors as rms_norm.
+ */
+int rms_norm_q8(const void *x, int type, size_t rows, size_t dim, size_t x_ld,
+                const void *residual, size_t residual_ld, const void *weight, int weight_type,
+                float eps, uint32_t group, uint8_t *codes, size_t codes_ld, float *scales, void *h,
+                size_t h_ld, float *rstd, void *stream);
+
+/*
+ * rms_norm_grad -- for the gradient dy of y (an 8-bit y passes it straight
+ * on) and the gradient dh that reaches h otherwise, in float32:
+ *     u = dy * weight
+ *     dx = rstd * (u - h * rstd^2 * mean(u * h)) + dh     (also the residual's)
+ *     dweight = sum over rows of dy * h * rstd            (+= with accumulate)
+ *
+ *   dy, h, dh  in,  rows x dim of `type`; h as rms_norm stored it (x without a
+ *              residual); dh may be NULL
+ *   rstd       in,  float32[rows] of rms_norm
+ *   dx         out, rows x dim of `type`; may be dh itself (same address, ld)
+ *   dweight    out, float32[dim]
+ *   work       rms_norm_work_bytes(rows, dim, type) bytes, 16-byte aligned,
+ *              contents not kept; calls that may run at the same time need
+ *              one each
+ *
+ * rows == 0 without accumulate zeroes dweight.
+ * Errors: as rms_norm.
+ */
+int rms_norm_grad(const void *dy, int type, size_t rows, size_t dim, size_t dy_ld, const void *h,
+                  size_t h_ld, const void *weight, int weight_type, const float *rstd,
+                  const void *dh, size_t dh_ld, void *dx, size_t dx_ld, float *dweight,
+                  int accumulate, void *work, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Distillation from a teacher's top logits                            */
+/* ------------------------------------------------------------------ */
+
+/*
+ * A teacher sends the k largest logits of each position instead of its whole
+ * row.  For a row with student logits z[0..vocab), temperature T and the
+ * teacher's entries (index a_j, logit t_j), an index outside [0, vocab)
+ * marking an absent entry, in float32:
+ *     p = softmax of t / T over the entries
+ *     q = softmax of z / T over the vocabulary,  lse = logsumexp(z / T)
+ *     loss = s * sum over j of p_j (log p_j - z[a_j] / T + lse)
+ *     dz_v = s / T * (q_v - sum of p_j over the j with a_j = v)
+ * with s = scale * row_scale[row] (scale alone for a NULL row_scale).
+ * Entries of probability 0 add nothing; an index may occur more than once.
+ *   - s = 0: the row is not read; loss, lse and dz are 0.
+ *   - no entry, or none but -inf: loss and dz are 0.
+ *   - no logit above -inf: lse is -inf, dz is 0 and the loss s * inf.
+ *   - NaN and +inf follow IEEE arithmetic.
+ *
+ *   logits     in,  rows x vocab of `type` (a float type)
+ *   index      in,  rows x k of index_type (GCQ_I32 or GCQ_I64)
+ *   teacher    in,  rows x k of teacher_type: `type` or GCQ_F32
+ *   k          1 .. GCQ_MAX_TOPK
+ *   T          finite and > 0;  scale finite
+ *   row_scale  in,  float32[rows], or NULL: a mask, a weight, or the
+ *              gradient that comes from above
+ *   loss, lse  out, float32[rows]
+ *   dlogits    out, rows x vocab of `type`; may be the logits themselves
+ *              (same address, ld)
+ *
+ * distill_loss gives loss and lse; distill_grad the gradient from a kept
+ * lse (distill_loss's for the same logits and T; rows with s = 0 ignore it);
+ * distill_loss_grad all three in one launch.
+ * vocab 1 .. GCQ_LM_MAX_DIM, rows <= GCQ_LM_MAX_ROWS.
+ * Errors: GCQ_ERR_PARAM, GCQ_ERR_NULL, GCQ_ERR_ALIGN, GCQ_ERR_OVERLAP,
+ * GCQ_ERR_LAUNCH.
+ */
+#define GCQ_MAX_TOPK 1024
+int distill_loss(const void *logits, int type, size_t rows, size_t vocab, size_t logits_ld,
+                 const void *index, int index_type, size_t index_ld, const void *teacher,
+                 int teacher_type, size_t teacher_ld, uint32_t k, float temperature,
+                 const float *row_scale, float scale, float *loss, float *lse, void *stream);
+int distill_grad(const void *logits, int type, size_t rows, size_t vocab, size_t logits_ld,
+                 const float *lse, const void *index, int index_type, size_t index_ld,
+                 const void *teacher, int teacher_type, size_t teacher_ld, uint32_t k,
+                 float temperature, const float *row_scale, float scale, void *dlogits,
+                 size_t dlogits_ld, void *stream);
+int distill_loss_grad(const void *logits, int type, size_t rows, size_t vocab, size_t logits_ld,
+                      const void *index, int index_type, size_t index_ld, const void *teacher,
+                      int teacher_type, size_t teacher_ld, uint32_t k, float temperature,
+                      const float *row_scale, float scale, float *loss, float *lse, void *dlogits,
+                      size_t dlogits_ld, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Sizes and status names (pure host functions, no device access)      */
 /* ------------------------------------------------------------------ */
 
@@ -555,6 +684,8 @@ size_t embed_plan_words(size_t n);
 /* Bytes of embed_grad's and embed_grad_rows' workspace (0 for sizes out of
  * range). */
 size_t embed_work_bytes(size_t n, size_t dim);
+/* Bytes of rms_norm_grad's workspace (0 for sizes or types out of range). */
+size_t rms_norm_work_bytes(size_t rows, size_t dim, int type);
 /* Static, never-NULL name of a status code. */
 const char *gcq_status_string(int status);
 
