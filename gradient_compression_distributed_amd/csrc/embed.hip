@@ -51,24 +51,70 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(const T *__restrict__
 }
 
 // -------------------------------------------------------------------- sort
-// Least-significant-digit radix sort of (token, position), digits of at most
-// 9 bits, tiles of 2048 positions.  A wavefront ranks 64 tokens at a time:
-// a ballot per digit bit gives each lane the lanes that share its digit, so
-// the rank is a count of lower lanes plus the wavefront's count so far, and
-// equal digits keep their order.
-constexpr uint32_t kDigitBits = 9, kBins = 1u << kDigitBits;
-constexpr uint32_t kSortThreads = 256, kSortItems = 8;
-constexpr uint32_t kSortTile = kSortThreads * kSortItems;
-// One workgroup sorts this many in LDS, in one launch.
-constexpr uint32_t kSmallThreads = 1024, kSmallItems = 4;
-constexpr uint32_t kSmallSort = kSmallThreads * kSmallItems;
-
-template <typename I>
-__device__ __forceinline__ uint32_t token_key(const I *tokens, uint64_t i, uint64_t vocab)
+__device__ __forceinline__ uint32_t key_of(int64_t token, uint64_t vocab)
 {
-    const uint64_t t = (uint64_t)(int64_t)((const GCQ_G I *)tokens)[i];
+    const uint64_t t = (uint64_t)token;
     return (uint32_t)(t < vocab ? t : vocab);   // padding sorts behind every token
 }
+
+// Few positions: each finds its place by counting.  The place of position i
+// is the number of positions before it with a key <= its own and of positions
+// behind it with a smaller key.  A workgroup holds every key in LDS; Ti lanes
+// take a position each, 1024 / Ti groups of lanes a share of the others.
+// n^2 comparisons (2 instructions each) cost less than the passes of a radix
+// sort, each of them bound by launch and latency, up to kCountSort positions.
+constexpr uint32_t kCountSort = 16384;
+template <typename I, uint32_t Ti>
+__global__ __launch_bounds__(1024) void embed_count_sort_kernel(const I *__restrict__ tokens,
+                                                                uint32_t n, uint32_t share,
+                                                                uint64_t vocab,
+                                                                uint32_t *__restrict__ keys,
+                                                                uint32_t *__restrict__ order)
+{
+    extern __shared__ __align__(16) uint32_t key_s[];   // share * 1024 / Ti keys, those past n never counted
+    __shared__ uint32_t place[Ti];
+    const uint32_t tid = threadIdx.x, all = share * (1024u / Ti);
+    for (uint32_t j = tid; j < all; j += 1024u)
+        key_s[j] = j < n ? key_of(((const GCQ_G I *)tokens)[j], vocab) : 0xFFFFFFFFu;
+    if (tid < Ti)
+        place[tid] = 0;
+    __syncthreads();
+    const uint32_t i0 = blockIdx.x * Ti, i = i0 + tid % Ti;
+    const uint32_t j0 = tid / Ti * share;
+    const uint32_t key = i < n ? key_s[i] : 0u;
+    uint32_t count = 0;
+    if (j0 + share <= i0 || j0 >= i0 + Ti) {
+        const uint32_t below = key + (j0 < i0);   // ahead: <= key; behind: < key
+#pragma unroll 4
+        for (uint32_t j = 0; j < share; j += 4) {
+            const uint4 k = *(const uint4 *)(key_s + j0 + j);
+            count += (uint32_t)(k.x < below) + (uint32_t)(k.y < below) + (uint32_t)(k.z < below) +
+                     (uint32_t)(k.w < below);
+        }
+    } else {
+        for (uint32_t j = j0; j < j0 + share; ++j)
+            count += key_s[j] < key + (j < i);
+    }
+    if (i < n)
+        atomicAdd(&place[tid % Ti], count);   // whole numbers: any order
+    __syncthreads();
+    if (tid < Ti && i < n && place[tid] < n) {
+        keys[place[tid]] = key;
+        order[place[tid]] = i;
+    }
+}
+
+// More: least-significant-digit radix sort of (key, position), digits of at
+// most 9 bits, tiles of 2048 positions, two launches a pass.  A wavefront
+// ranks 64 keys at a time: a ballot per digit bit gives each lane the lanes
+// that share its digit, so the rank is a count of lower lanes plus the
+// wavefront's count so far, and equal digits keep their order.
+constexpr uint32_t kDigitBits = 9, kBins = 1u << kDigitBits;
+constexpr uint32_t kSortThreads = 512, kSortItems = 4;
+constexpr uint32_t kSortTile = kSortThreads * kSortItems;
+// Up to this many tiles each scatter sums the tiles' counts itself; beyond, a
+// launch of its own scans them (a scatter's own reading grows with the square).
+constexpr uint32_t kSumTiles = 128;
 
 __device__ __forceinline__ void wave_order()
 {
@@ -80,29 +126,35 @@ __device__ __forceinline__ void wave_order()
 // Ranks this wavefront's Items digits among its earlier ones of equal value;
 // cnt[bin] (zero on entry) ends as the wavefront's histogram.  Items with
 // digit >= kBins take no part.
-template <int Items, typename C>
-__device__ __forceinline__ void wave_rank(const uint32_t (&digit)[Items], uint32_t bits, C *cnt,
-                                          uint32_t (&rank)[Items])
+template <int Items>
+__device__ __forceinline__ void wave_rank(const uint32_t (&digit)[Items], uint32_t bits,
+                                          uint32_t *cnt, uint32_t (&rank)[Items])
 {
     const uint32_t lane = threadIdx.x & (kWave - 1);
     const uint64_t below = (1ull << lane) - 1u;
+    uint64_t peers[Items];
+#pragma unroll
+    for (int j = 0; j < Items; ++j)
+        peers[j] = __ballot(digit[j] < kBins);
+    for (uint32_t b = 0; b < bits; ++b) {
+#pragma unroll
+        for (int j = 0; j < Items; ++j) {
+            const bool one = (digit[j] >> b) & 1u;
+            const uint64_t m = __ballot(one);
+            peers[j] &= one ? m : ~m;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < Items; ++j) {
         const bool in = digit[j] < kBins;
-        uint64_t peers = __ballot(in);
-        for (uint32_t b = 0; b < bits; ++b) {
-            const bool one = (digit[j] >> b) & 1u;
-            const uint64_t m = __ballot(one);
-            peers &= one ? m : ~m;
-        }
         uint32_t first = 0;
         if (in)
             first = cnt[digit[j]];
         wave_order();   // every lane has read before the count moves
-        if (in && (peers & below) == 0)
-            cnt[digit[j]] = (C)(first + (uint32_t)__popcll(peers));
+        if (in && (peers[j] & below) == 0)
+            cnt[digit[j]] = first + (uint32_t)__popcll(peers[j]);
         wave_order();
-        rank[j] = first + (uint32_t)__popcll(peers & below);
+        rank[j] = first + (uint32_t)__popcll(peers[j] & below);
     }
 }
 
@@ -138,107 +190,168 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t *sums, uint3
     return before + incl - x;
 }
 
-template <typename I>
-__global__ __launch_bounds__(kSmallThreads) void embed_sort_small_kernel(
-    const I *__restrict__ tokens, uint32_t n, uint64_t vocab, uint32_t bits, uint32_t digit_bits,
-    uint32_t *__restrict__ keys, uint32_t *__restrict__ order)
-{
-    constexpr uint32_t waves = kSmallThreads / kWave;
-    __shared__ uint32_t key_s[kSmallSort];
-    __shared__ uint16_t pos_s[kSmallSort];
-    __shared__ uint16_t cnt[waves][kBins];
-    __shared__ uint32_t base[kBins], sums[waves];
-    const uint32_t tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const uint32_t at = wave * kWave * kSmallItems + lane;   // item j: at + 64 j
-    uint32_t key[kSmallItems], pos[kSmallItems], rank[kSmallItems], digit[kSmallItems];
-#pragma unroll
-    for (uint32_t j = 0; j < kSmallItems; ++j) {
-        pos[j] = at + kWave * j;
-        key[j] = pos[j] < n ? token_key(tokens, pos[j], vocab) : 0u;
-    }
-    for (uint32_t shift = 0; shift < bits; shift += digit_bits) {
-        for (uint32_t i = tid; i < waves * kBins; i += kSmallThreads)
-            (&cnt[0][0])[i] = 0;
-        __syncthreads();
-        const uint32_t mask = (1u << digit_bits) - 1u;
-#pragma unroll
-        for (uint32_t j = 0; j < kSmallItems; ++j)
-            digit[j] = at + kWave * j < n ? (key[j] >> shift) & mask : kBins;
-        wave_rank<kSmallItems>(digit, digit_bits, cnt[wave], rank);
-        __syncthreads();
-        uint32_t mine = 0;   // bin tid: this workgroup's count, each wavefront's start
-        if (tid < kBins) {
-            for (uint32_t w = 0; w < waves; ++w) {
-                const uint32_t c = cnt[w][tid];
-                cnt[w][tid] = (uint16_t)mine;
-                mine += c;
-            }
-        }
-        uint32_t total;
-        const uint32_t first = block_scan<kSmallThreads>(mine, sums, total);
-        if (tid < kBins)
-            base[tid] = first;
-        __syncthreads();
-#pragma unroll
-        for (uint32_t j = 0; j < kSmallItems; ++j) {
-            if (digit[j] < kBins) {
-                const uint32_t to = base[digit[j]] + cnt[wave][digit[j]] + rank[j];
-                key_s[to] = key[j];
-                pos_s[to] = (uint16_t)pos[j];
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (uint32_t j = 0; j < kSmallItems; ++j) {
-            const uint32_t i = at + kWave * j;
-            if (i < n) {
-                key[j] = key_s[i];
-                pos[j] = pos_s[i];
-            }
-        }
-        // the next pass's barriers come between these reads and its writes
-    }
-#pragma unroll
-    for (uint32_t j = 0; j < kSmallItems; ++j) {
-        const uint32_t i = at + kWave * j;
-        if (i < n) {
-            keys[i] = key[j];
-            order[i] = pos[j];
-        }
-    }
-}
-
-// The tile's digit counts, digit-major: hist[digit * tiles + tile].
-// First: keys come from the tokens.
+// The tile's digit counts: hist[tile][digit].  First: keys come from the
+// tokens.
 template <typename I, bool First>
 __global__ __launch_bounds__(kSortThreads) void embed_hist_kernel(
     const I *__restrict__ tokens, const uint32_t *__restrict__ keys, uint32_t n, uint64_t vocab,
-    uint32_t shift, uint32_t digit_bits, uint32_t *__restrict__ hist, uint32_t tiles)
+    uint32_t shift, uint32_t digit_bits, uint32_t *__restrict__ hist)
 {
     __shared__ uint32_t cnt[kBins];
-    const uint32_t bins = 1u << digit_bits, tid = threadIdx.x;
-    for (uint32_t i = tid; i < bins; i += kSortThreads)
-        cnt[i] = 0;
-    __syncthreads();
+    static_assert(kBins == kSortThreads, "a thread per digit");
+    const uint32_t mask = (1u << digit_bits) - 1u, tid = threadIdx.x;
     const uint64_t t0 = (uint64_t)blockIdx.x * kSortTile;
+    uint32_t k[kSortItems];
 #pragma unroll
     for (uint32_t j = 0; j < kSortItems; ++j) {
         const uint64_t i = t0 + tid + kSortThreads * j;
-        if (i < n) {
-            const uint32_t k = First ? token_key(tokens, i, vocab) : keys[i];
-            atomicAdd(&cnt[(k >> shift) & (bins - 1u)], 1u);   // whole numbers: any order
-        }
+        k[j] = i >= n ? 0u : First ? key_of(((const GCQ_G I *)tokens)[i], vocab) : keys[i];
     }
+    cnt[tid] = 0;
     __syncthreads();
-    for (uint32_t i = tid; i < bins; i += kSortThreads)
-        hist[(uint64_t)i * tiles + blockIdx.x] = cnt[i];
+#pragma unroll
+    for (uint32_t j = 0; j < kSortItems; ++j)
+        if (t0 + tid + kSortThreads * j < n)
+            atomicAdd(&cnt[(k[j] >> shift) & mask], 1u);   // whole numbers: any order
+    __syncthreads();
+    hist[(uint64_t)blockIdx.x * kBins + tid] = cnt[tid];
 }
 
-// In-place exclusive scan of a[0..m) by one workgroup, the total to a[m] if
-// `put_total`.
+// In place per digit: each tile's count becomes the count in earlier tiles,
+// the row behind the tiles the digit's total.  64 digits per workgroup, 16
+// threads a digit over consecutive shares of the tiles.
+__global__ __launch_bounds__(1024) void embed_hist_scan_kernel(uint32_t *__restrict__ hist,
+                                                               uint32_t tiles)
+{
+    __shared__ uint32_t share[16][kWave];
+    const uint32_t lane = threadIdx.x & (kWave - 1), part = threadIdx.x / kWave;
+    uint32_t *h = hist + blockIdx.x * kWave + lane;
+    const uint32_t each = (tiles + 15u) / 16u;
+    const uint32_t t0 = part * each < tiles ? part * each : tiles;
+    const uint32_t t1 = t0 + each < tiles ? t0 + each : tiles;
+    uint32_t sum = 0;
+#pragma unroll 8
+    for (uint32_t t = t0; t < t1; ++t)
+        sum += h[(uint64_t)t * kBins];
+    share[part][lane] = sum;
+    __syncthreads();
+    uint32_t x = 0, all = 0;
+    for (uint32_t p = 0; p < 16; ++p) {
+        x += p < part ? share[p][lane] : 0u;
+        all += share[p][lane];
+    }
+    for (uint32_t t = t0; t < t1; ++t) {
+        const uint32_t v = h[(uint64_t)t * kBins];
+        h[(uint64_t)t * kBins] = x;
+        x += v;
+    }
+    if (part == 0)
+        h[(uint64_t)tiles * kBins] = all;
+}
+
+// Scanned: the counts went through embed_hist_scan_kernel.
+template <typename I, bool First, bool Scanned>
+__global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(
+    const I *__restrict__ tokens, const uint32_t *__restrict__ keys_in,
+    const uint32_t *__restrict__ order_in, uint32_t n, uint64_t vocab, uint32_t shift,
+    uint32_t digit_bits, const uint32_t *__restrict__ hist, uint32_t tiles,
+    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ order_out)
+{
+    constexpr uint32_t waves = kSortThreads / kWave;
+    __shared__ uint32_t cnt[waves][kBins], sums[waves];
+    const uint32_t mask = (1u << digit_bits) - 1u, tid = threadIdx.x;
+    const uint32_t lane = tid & (kWave - 1), wave = tid / kWave;
+    const uint64_t at = (uint64_t)blockIdx.x * kSortTile + wave * kWave * kSortItems + lane;
+    uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems], digit[kSortItems];
+#pragma unroll
+    for (uint32_t j = 0; j < kSortItems; ++j) {
+        const uint64_t i = at + kWave * j;
+        key[j] = 0;
+        pos[j] = (uint32_t)i;
+        if (i < n) {
+            key[j] = First ? key_of(((const GCQ_G I *)tokens)[i], vocab) : keys_in[i];
+            if (!First)
+                pos[j] = order_in[i];
+        }
+    }
+    // digit tid: its count in all tiles, and in earlier ones
+    uint32_t before = 0, all = 0;
+    if constexpr (Scanned) {
+        before = hist[(uint64_t)blockIdx.x * kBins + tid];
+        all = hist[(uint64_t)tiles * kBins + tid];
+    } else {
+#pragma unroll 16
+        for (uint32_t t = 0; t < tiles; ++t) {
+            const uint32_t c = hist[(uint64_t)t * kBins + tid];
+            before += t < blockIdx.x ? c : 0u;
+            all += c;
+        }
+    }
+#pragma unroll
+    for (uint32_t w = 0; w < waves; ++w)
+        cnt[w][tid] = 0;
+    uint32_t total;
+    before += block_scan<kSortThreads>(all, sums, total);   // and a barrier
+#pragma unroll
+    for (uint32_t j = 0; j < kSortItems; ++j)
+        digit[j] = at + kWave * j < n ? (key[j] >> shift) & mask : kBins;
+    wave_rank<kSortItems>(digit, digit_bits, cnt[wave], rank);
+    __syncthreads();
+    uint32_t c[waves];
+#pragma unroll
+    for (uint32_t w = 0; w < waves; ++w)
+        c[w] = cnt[w][tid];
+#pragma unroll
+    for (uint32_t w = 0; w < waves; ++w) {
+        cnt[w][tid] = before;
+        before += c[w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t j = 0; j < kSortItems; ++j) {
+        if (digit[j] < kBins) {
+            const uint32_t to = cnt[wave][digit[j]] + rank[j];
+            if (to < n) {
+                keys_out[to] = key[j];
+                order_out[to] = pos[j];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gradient
+// Segment starts before each run of sorted positions (within its tile), and
+// each tile's count.
+__global__ __launch_bounds__(256) void embed_starts_kernel(const uint32_t *__restrict__ keys,
+                                                           uint32_t n, uint32_t vocab, uint32_t run,
+                                                           uint32_t *__restrict__ starts,
+                                                           uint32_t *__restrict__ tiles)
+{
+    __shared__ uint32_t sums[256 / kWave];
+    constexpr uint32_t per = kEmbedTile / 256u;
+    const uint64_t i0 = (uint64_t)blockIdx.x * kEmbedTile + threadIdx.x * per;
+    uint32_t mine = 0;
+    uint32_t last = i0 && i0 < n ? keys[i0 - 1] : 0xFFFFFFFFu;
+#pragma unroll
+    for (uint32_t j = 0; j < per; ++j) {
+        if (i0 + j < n) {
+            const uint32_t k = keys[i0 + j];
+            mine += k != last && k < vocab;
+            last = k;
+        }
+    }
+    uint32_t total;
+    const uint32_t before = block_scan<256>(mine, sums, total);
+    if (i0 < n && i0 % run == 0)
+        starts[i0 / run] = before;
+    if (threadIdx.x == 0)
+        tiles[blockIdx.x] = total;
+}
+
+// In-place exclusive scan of a[0..m) by one workgroup, the total to a[m].
 constexpr uint32_t kScanThreads = 1024, kScanItems = 8;
 __global__ __launch_bounds__(kScanThreads) void embed_scan_kernel(uint32_t *__restrict__ a,
-                                                                  uint64_t m, bool put_total)
+                                                                  uint64_t m)
 {
     __shared__ uint32_t sums[kScanThreads / kWave];
     uint32_t carry = 0;
@@ -259,148 +372,151 @@ __global__ __launch_bounds__(kScanThreads) void embed_scan_kernel(uint32_t *__re
         }
         carry += total;
     }
-    if (put_total && threadIdx.x == 0)
-        a[m] = carry;
-}
-
-template <typename I, bool First>
-__global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(
-    const I *__restrict__ tokens, const uint32_t *__restrict__ keys_in,
-    const uint32_t *__restrict__ order_in, uint32_t n, uint64_t vocab, uint32_t shift,
-    uint32_t digit_bits, const uint32_t *__restrict__ hist, uint32_t tiles,
-    uint32_t *__restrict__ keys_out, uint32_t *__restrict__ order_out)
-{
-    constexpr uint32_t waves = kSortThreads / kWave;
-    __shared__ uint32_t cnt[waves][kBins];
-    const uint32_t bins = 1u << digit_bits, tid = threadIdx.x;
-    const uint32_t lane = tid & (kWave - 1), wave = tid / kWave;
-    for (uint32_t i = tid; i < waves * kBins; i += kSortThreads)
-        (&cnt[0][0])[i] = 0;
-    __syncthreads();
-    const uint64_t at = (uint64_t)blockIdx.x * kSortTile + wave * kWave * kSortItems + lane;
-    uint32_t key[kSortItems], pos[kSortItems], rank[kSortItems], digit[kSortItems];
-#pragma unroll
-    for (uint32_t j = 0; j < kSortItems; ++j) {
-        const uint64_t i = at + kWave * j;
-        key[j] = 0;
-        pos[j] = (uint32_t)i;
-        if (i < n) {
-            key[j] = First ? token_key(tokens, i, vocab) : keys_in[i];
-            if (!First)
-                pos[j] = order_in[i];
-        }
-        digit[j] = i < n ? (key[j] >> shift) & (bins - 1u) : kBins;
-    }
-    wave_rank<kSortItems>(digit, digit_bits, cnt[wave], rank);
-    __syncthreads();
-    for (uint32_t b = tid; b < bins; b += kSortThreads) {
-        uint32_t first = hist[(uint64_t)b * tiles + blockIdx.x];
-        for (uint32_t w = 0; w < waves; ++w) {
-            const uint32_t c = cnt[w][b];
-            cnt[w][b] = first;
-            first += c;
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (uint32_t j = 0; j < kSortItems; ++j) {
-        if (digit[j] < kBins) {
-            const uint32_t to = cnt[wave][digit[j]] + rank[j];
-            if (to < n) {
-                keys_out[to] = key[j];
-                order_out[to] = pos[j];
-            }
-        }
-    }
-}
-
-// ---------------------------------------------------------------- gradient
-// Segment starts before each run of kEmbedRun sorted positions (within its
-// tile), and each tile's count.
-__global__ __launch_bounds__(256) void embed_starts_kernel(const uint32_t *__restrict__ keys,
-                                                           uint32_t n, uint32_t vocab,
-                                                           uint32_t *__restrict__ starts,
-                                                           uint32_t *__restrict__ tiles)
-{
-    __shared__ uint32_t sums[256 / kWave];
-    constexpr uint32_t per = kEmbedTile / 256u;
-    const uint64_t i0 = (uint64_t)blockIdx.x * kEmbedTile + threadIdx.x * per;
-    uint32_t mine = 0;
-    uint32_t last = i0 && i0 < n ? keys[i0 - 1] : 0xFFFFFFFFu;
-#pragma unroll
-    for (uint32_t j = 0; j < per; ++j) {
-        if (i0 + j < n) {
-            const uint32_t k = keys[i0 + j];
-            mine += k != last && k < vocab;
-            last = k;
-        }
-    }
-    uint32_t total;
-    const uint32_t before = block_scan<256>(mine, sums, total);
-    if (i0 < n && i0 % kEmbedRun == 0)
-        starts[i0 / kEmbedRun] = before;
     if (threadIdx.x == 0)
-        tiles[blockIdx.x] = total;
+        a[m] = carry;
 }
 
 enum class Form { kWrite, kAdd, kRows };
 
-// Where a finished sum goes.
+// Zeroes the rows [v0, v0 + 64) of the dense gradient that no position names.
+// 128 threads each search for the first position of a row >= v0 and of one
+// >= v0 + 64, a 128th of the range at a time; the positions between name the
+// rows to leave.
+constexpr uint32_t kZeroRows = 64;
+__device__ __forceinline__ void zero_rows(const EmbedGrad &e, uint64_t v0)
+{
+    __shared__ uint32_t votes[4];
+    __shared__ unsigned long long named;
+    const uint32_t tid = threadIdx.x, side = tid / 128u;
+    const uint64_t target = v0 + (side ? kZeroRows : 0u);
+    uint64_t lo[2] = {0, 0}, hi[2] = {e.n, e.n};
+    if (tid == 0)
+        named = 0;
+    while (lo[0] < hi[0] || lo[1] < hi[1]) {
+        const uint64_t step = (hi[side] - lo[side] + 127u) / 128u;
+        const uint64_t at = lo[side] + (tid % 128u) * step;
+        const uint64_t m = __ballot(at < hi[side] && e.keys[at] < target);
+        if ((tid & (kWave - 1)) == 0)
+            votes[tid / kWave] = (uint32_t)__popcll(m);
+        __syncthreads();
+#pragma unroll
+        for (uint32_t s = 0; s < 2; ++s) {
+            const uint32_t below = votes[2 * s] + votes[2 * s + 1];   // probes below the target
+            const uint64_t st = (hi[s] - lo[s] + 127u) / 128u;
+            const uint64_t end = lo[s] + below * st;
+            hi[s] = end < hi[s] ? end : hi[s];
+            lo[s] = below ? lo[s] + (below - 1u) * st + 1u : lo[s];
+            if (!below)
+                hi[s] = lo[s];
+        }
+        __syncthreads();
+    }
+    __syncthreads();   // named is 0
+    const uint64_t a = lo[0], b = lo[1];
+    if (b - a <= 1024u) {
+        uint64_t mine = 0;
+        for (uint64_t i = a + tid; i < b; i += 256u)
+            mine |= 1ull << (e.keys[i] - v0);
+        if (mine)
+            atomicOr(&named, (unsigned long long)mine);
+    } else if (tid < kZeroRows) {   // long segments: each row looks for its first position
+        uint64_t l = a, h = b;
+        while (l < h) {
+            const uint64_t mid = (l + h) / 2;
+            if (e.keys[mid] < v0 + tid)
+                l = mid + 1;
+            else
+                h = mid;
+        }
+        const uint64_t m = __ballot(l < b && e.keys[l] == v0 + tid);
+        if (tid == 0)
+            named = m;
+    }
+    __syncthreads();
+    const uint64_t rows = e.vocab - v0 < kZeroRows ? e.vocab - v0 : kZeroRows;
+    uint64_t m = ~(uint64_t)named;
+    if (rows < 64)
+        m &= (1ull << rows) - 1u;
+    const vec<float, 4> zero = 0.0f;
+    for (; m; m &= m - 1) {
+        float *row = e.out + (v0 + (uint64_t)__builtin_ctzll(m)) * e.out_ld;
+        for (uint64_t c = tid * 4u; c < e.dim; c += 1024u)
+            store_vec<float, 4>(row + c, zero, (int64_t)(e.dim - c));
+    }
+}
+
+// Where a finished sum goes; `old` is what is there (kAdd).
 template <Form F, int N>
 __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64_t c,
-                                        fvec<N> acc, int64_t left)
+                                        fvec<N> acc, fvec<N> old, int64_t left)
 {
-    float *p = e.out + row * e.out_ld + c;
     fvec<N> v = acc * e.scale;
     if constexpr (F == Form::kAdd)
-        v += load_vec<float, N>(p, left);
-    store_vec<float, N>(p, v, left);
+        v += old;
+    store_vec<float, N>(e.out + row * e.out_ld + c, v, left);
 }
 
 // One pass over g in sorted order.  L lanes (a power of two up to 256) share
-// a run of 32 sorted positions and L * N columns.  A segment inside the run
-// is finished here; one that reaches over an end leaves its sum in
-// part[run][0] (it began before the run) or part[run][1].
+// a run of e.run sorted positions and L * N columns.  A segment inside the
+// run is finished here; one that reaches over an end leaves its sum in
+// part[run][0] (it began before the run) or part[run][1].  kWrite: the
+// workgroups behind the first `blocks` zero the rows that no position names.
 template <typename T, Form F>
-__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t lanes)
+__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t lanes, uint32_t cols,
+                                                         uint64_t blocks)
 {
-    constexpr int N = kVec<T>, U = 8;
-    __shared__ uint32_t key_s[32][kEmbedRun + 2], pos_s[32][kEmbedRun];
+    constexpr int N = kVec<T>, U = 4;
+    const uint64_t block = block_number();
+    if constexpr (F == Form::kWrite) {
+        if (block >= blocks) {
+            const uint64_t v0 = (block - blocks) * kZeroRows;
+            if (v0 < e.vocab)
+                zero_rows(e, v0);
+            return;
+        }
+    }
+    __shared__ uint32_t key_s[32 * (kEmbedRun + 2)], pos_s[32 * kEmbedRun];
     const uint32_t groups = 256u / lanes, lane = threadIdx.x & (lanes - 1);
-    const uint32_t slot = threadIdx.x / lanes;
-    const uint64_t run0 = (uint64_t)blockIdx.x * groups;
+    const uint32_t slot = threadIdx.x / lanes, R = e.run;
+    const uint64_t run0 = block / cols * groups;
     const uint64_t n = e.n;
     // key_s[s][1 + i]: the run's keys, with one neighbour on each side
     // (beyond the ends: no key at all, 2^32 - 1)
-    for (uint32_t i = threadIdx.x; i < groups * (kEmbedRun + 2); i += 256u) {
-        const uint32_t s = i / (kEmbedRun + 2), j = i % (kEmbedRun + 2);
-        const uint64_t at = (run0 + s) * kEmbedRun + j;   // one past the position
-        key_s[s][j] = at >= 1 && at <= n ? e.keys[at - 1] : 0xFFFFFFFFu;
-        if (j < kEmbedRun && at < n)
-            pos_s[s][j] = e.order[at];
+    for (uint32_t i = threadIdx.x; i < groups * (R + 2); i += 256u) {
+        const uint32_t s = i / (R + 2), j = i % (R + 2);
+        const uint64_t at = (run0 + s) * R + j;   // one past the position
+        key_s[i] = at >= 1 && at <= n ? e.keys[at - 1] : 0xFFFFFFFFu;
+        if (j < R)
+            pos_s[s * R + j] = at < n ? e.order[at] : 0u;
     }
     __syncthreads();
-    const uint64_t run = run0 + slot, i0 = run * kEmbedRun;
-    const uint64_t c = ((uint64_t)blockIdx.y * lanes + lane) * N;
+    const uint64_t run = run0 + slot, i0 = run * R;
+    const uint64_t c = (block % cols * lanes + lane) * N;
     if (i0 >= n || c >= e.dim)
         return;
-    const uint32_t len = n - i0 < kEmbedRun ? (uint32_t)(n - i0) : kEmbedRun;
-    const uint32_t *key = key_s[slot] + 1;
+    const uint32_t len = n - i0 < R ? (uint32_t)(n - i0) : R;
+    const uint32_t *key = key_s + slot * (R + 2) + 1, *pos = pos_s + slot * R;
     const int64_t left = (int64_t)(e.dim - c);
     const T *g = (const T *)e.g + c;
     uint64_t seat = 0;
     if constexpr (F == Form::kRows)
         seat = (uint64_t)e.tiles[i0 / kEmbedTile] + e.starts[run] - 1u;   // of the segment open here
+    const bool heads = key[0] == key[-1];   // the first segment began before the run
     fvec<N> acc = 0.0f;
     for (uint32_t b = 0; b < len; b += U) {
         vec<T, N> v[U];
+        fvec<N> old[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
+            const uint32_t i = b + j;
             v[j] = (T)0.0f;
-            if (b + j < len && key[b + j] < e.vocab) {
-                const uint64_t at = pos_s[slot][b + j];
-                if (at < n)
-                    v[j] = load_vec<T, N>(g + at * e.ld, left);
+            old[j] = 0.0f;
+            if (i < len && key[i] < e.vocab) {
+                if (pos[i] < n)
+                    v[j] = load_vec<T, N>(g + pos[i] * e.ld, left);
+                if constexpr (F == Form::kAdd)
+                    if (key[i] != key[i + 1])
+                        old[j] = load_vec<float, N>(e.out + key[i] * e.out_ld + c, left);
             }
         }
 #pragma unroll
@@ -411,7 +527,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t l
             const uint32_t k = key[i];
             if (k >= e.vocab)
                 break;   // padding: so is everything behind it
-            const bool opens = k != key_s[slot][i];
+            const bool opens = k != key[(int)i - 1];
             if constexpr (F == Form::kRows) {
                 if (opens) {
                     ++seat;
@@ -424,10 +540,9 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t l
             const bool closes = k != key[i + 1];
             if (!closes && i + 1 < len)
                 continue;
-            // did this segment begin before the run?
-            const bool head = key[0] == k && key_s[slot][0] == k;
+            const bool head = heads && key[0] == k;
             if (closes && !head) {
-                put_row<F, N>(e, F == Form::kRows ? seat : k, c, acc, left);
+                put_row<F, N>(e, F == Form::kRows ? seat : k, c, acc, old[j], left);
             } else {
                 float *p = e.part + (2 * run + (head ? 0 : 1)) * e.dim + c;
                 store_vec<float, N>(p, acc, left);
@@ -441,90 +556,88 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t l
 }
 
 // Joins the segments that reach over the end of the run they begin in: part
-// 1 of that run, then part 0 of the following ones, summed by 8 wavefronts
-// over consecutive shares and the shares in order.
-constexpr uint32_t kJoinThreads = 512, kJoinRuns = 4;
+// 1 of that run, then part 0 of the following ones.  A workgroup looks at 16
+// runs and 256 columns; a wavefront adds up a segment of at most kJoinShort
+// parts by itself, longer ones are shared by all 8 (consecutive parts each,
+// their sums added in order).
+constexpr uint32_t kJoinThreads = 512, kJoinRuns = 16, kJoinShort = 16;
 template <Form F>
-__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, uint32_t runs)
+__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, uint64_t runs)
 {
     constexpr int N = 4;
     constexpr uint32_t waves = kJoinThreads / kWave;
     __shared__ fvec<N> share[waves][kWave];
-    const uint32_t lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+    const uint32_t lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, R = e.run;
     const uint64_t c = ((uint64_t)blockIdx.y * kWave + lane) * N;
     const int64_t left = c < e.dim ? (int64_t)(e.dim - c) : 0;
-    for (uint32_t q = 0; q < kJoinRuns; ++q) {
-        const uint64_t run = (uint64_t)blockIdx.x * kJoinRuns + q;
-        const uint64_t i0 = run * kEmbedRun, end = i0 + kEmbedRun;
-        if (run >= runs || end >= e.n)
-            return;
-        const uint32_t k = e.keys[end - 1];
-        if (k >= e.vocab || k != e.keys[end])
-            continue;   // nothing reaches over
-        if (i0 && e.keys[i0 - 1] == k)
-            continue;   // it began earlier: an earlier run joins it
-        uint64_t lo = end, hi = e.n;   // the first position behind the segment
-        while (lo < hi) {
-            const uint64_t mid = (lo + hi) / 2;
-            if (e.keys[mid] == k)
-                lo = mid + 1;
-            else
-                hi = mid;
+    const uint64_t run0 = (uint64_t)blockIdx.x * kJoinRuns;
+    // every wavefront: which of the runs begin a segment that reaches over
+    // their end, and with which key
+    bool joins = false;
+    uint32_t k0 = 0;
+    {
+        const uint64_t end = (run0 + lane + 1) * R;
+        if (lane < kJoinRuns && end < e.n) {
+            k0 = e.keys[end - 1];
+            const uint64_t i0 = end - R;
+            const uint32_t next = e.keys[end], prev = i0 ? e.keys[i0 - 1] : 0xFFFFFFFFu;
+            joins = k0 < e.vocab && next == k0 && prev != k0;
         }
-        const uint64_t parts = (lo - 1) / kEmbedRun - run + 1;   // runs it touches
-        const uint64_t each = (parts + waves - 1) / waves;
-        const uint64_t p0 = wave * each, p1 = p0 + each < parts ? p0 + each : parts;
+    }
+    uint32_t turn = 0;
+    for (uint64_t m = __ballot(joins); m; m &= m - 1, ++turn) {
+        const uint32_t q = (uint32_t)__builtin_ctzll(m);
+        const uint32_t k = (uint32_t)__shfl((int)k0, (int)q, kWave);
+        const uint64_t run = run0 + q;
+        // the following runs that it opens: 64 at a time
+        uint64_t parts = 1;
+        for (;;) {
+            const uint64_t at = (run + parts + lane) * R;
+            const uint64_t goes = __ballot(at < e.n && e.keys[at] == k);
+            const uint32_t more = ~goes ? (uint32_t)__builtin_ctzll(~goes) : 64u;
+            parts += more;
+            if (more < 64)
+                break;
+        }
+        const bool alone = parts <= kJoinShort;
+        if (alone && turn % waves != wave)
+            continue;
+        fvec<N> old = 0.0f;
+        uint64_t row = k;
+        if constexpr (F == Form::kRows) {
+            // the last segment that opens in this run
+            bool opens = false;
+            if (lane < R) {
+                const uint64_t i = run * R + lane;
+                opens = i == 0 || e.keys[i] != e.keys[i - 1];
+            }
+            row = (uint64_t)e.tiles[run * R / kEmbedTile] + e.starts[run] +
+                  (uint32_t)__popcll(__ballot(opens)) - 1u;
+        }
+        if constexpr (F == Form::kAdd)
+            if (left > 0)
+                old = load_vec<float, N>(e.out + row * e.out_ld + c, left);
+        const uint64_t each = alone ? parts : (parts + waves - 1) / waves;
+        const uint64_t p0 = alone ? 0 : wave * each, p1 = p0 + each < parts ? p0 + each : parts;
         fvec<N> acc = 0.0f;
         if (left > 0) {
 #pragma unroll 8
             for (uint64_t p = p0; p < p1; ++p)
                 acc += load_vec<float, N>(e.part + (2 * (run + p) + (p ? 0 : 1)) * e.dim + c, left);
         }
+        if (alone) {
+            if (left > 0)
+                put_row<F, N>(e, row, c, acc, old, left);
+            continue;
+        }
+        __syncthreads();   // share may still be read
         share[wave][lane] = acc;
         __syncthreads();
         if (wave == 0 && left > 0) {
             for (uint32_t w = 1; w < waves && w * each < parts; ++w)
                 acc += share[w][lane];
-            uint64_t row = k;
-            if constexpr (F == Form::kRows) {
-                // the last segment that opens in this run
-                uint32_t opens = 0;
-                for (uint32_t i = 0; i < kEmbedRun; ++i)
-                    opens += i0 + i == 0 || e.keys[i0 + i] != e.keys[i0 + i - 1];
-                row = (uint64_t)e.tiles[i0 / kEmbedTile] + e.starts[run] + opens - 1u;
-            }
-            put_row<F, N>(e, row, c, acc, left);
+            put_row<F, N>(e, row, c, acc, old, left);
         }
-        __syncthreads();
-    }
-}
-
-// Zeroes the rows of the dense gradient that no position names: 64 rows per
-// workgroup, one lane each looks its row up in the sorted tokens.
-__global__ __launch_bounds__(256) void embed_zero_kernel(EmbedGrad e)
-{
-    __shared__ uint64_t untouched;
-    const uint64_t v0 = block_number() * kWave;
-    if (threadIdx.x < kWave) {
-        const uint64_t v = v0 + threadIdx.x;
-        uint64_t lo = 0, hi = e.n;
-        while (lo < hi) {
-            const uint64_t mid = (lo + hi) / 2;
-            if (e.keys[mid] < v)
-                lo = mid + 1;
-            else
-                hi = mid;
-        }
-        const uint64_t m = __ballot(v < e.vocab && !(lo < e.n && e.keys[lo] == v));
-        if (threadIdx.x == 0)
-            untouched = m;
-    }
-    __syncthreads();
-    const vec<float, 4> zero = 0.0f;
-    for (uint64_t m = untouched; m; m &= m - 1) {
-        float *row = e.out + (v0 + (uint64_t)__builtin_ctzll(m)) * e.out_ld;
-        for (uint64_t c = threadIdx.x * 4u; c < e.dim; c += 1024u)
-            store_vec<float, 4>(row + c, zero, (int64_t)(e.dim - c));
     }
 }
 
@@ -570,39 +683,61 @@ hipError_t lookup(const EmbedTable &t, const void *tokens, uint64_t n, float sca
     }
 }
 
+template <typename I, uint32_t Ti>
+void count_sort(const I *tokens, uint32_t n, uint64_t vocab, uint32_t *keys, uint32_t *order,
+                hipStream_t s)
+{
+    const uint32_t groups = 1024u / Ti, share = ((n + groups - 1) / groups + 3u) / 4u * 4u;
+    embed_count_sort_kernel<I, Ti><<<(n + Ti - 1) / Ti, 1024, 4 * share * groups, s>>>(
+        tokens, n, share, vocab, keys, order);
+}
+
+template <typename I, bool First>
+void sort_pass(const I *tokens, const uint32_t *keys_in, const uint32_t *order_in, uint32_t n,
+               uint64_t vocab, uint32_t shift, uint32_t digit, uint32_t *hist, uint32_t tiles,
+               uint32_t *keys_out, uint32_t *order_out, hipStream_t s)
+{
+    embed_hist_kernel<I, First>
+        <<<tiles, kSortThreads, 0, s>>>(tokens, keys_in, n, vocab, shift, digit, hist);
+    if (tiles <= kSumTiles) {
+        embed_scatter_kernel<I, First, false><<<tiles, kSortThreads, 0, s>>>(
+            tokens, keys_in, order_in, n, vocab, shift, digit, hist, tiles, keys_out, order_out);
+    } else {
+        embed_hist_scan_kernel<<<kBins / kWave, 1024, 0, s>>>(hist, tiles);
+        embed_scatter_kernel<I, First, true><<<tiles, kSortThreads, 0, s>>>(
+            tokens, keys_in, order_in, n, vocab, shift, digit, hist, tiles, keys_out, order_out);
+    }
+}
+
 template <typename I>
 hipError_t sort_tokens(const I *tokens, uint32_t n, uint64_t vocab, uint32_t *plan, hipStream_t s)
 {
+    uint32_t *keys[2] = {plan, plan + 2 * (uint64_t)n};
+    uint32_t *order[2] = {plan + n, plan + 3 * (uint64_t)n};
+    if (n <= kCountSort) {   // 256 workgroups or more where the positions allow it
+        if (n <= 4096)
+            count_sort<I, 16>(tokens, n, vocab, keys[0], order[0], s);
+        else if (n <= 8192)
+            count_sort<I, 32>(tokens, n, vocab, keys[0], order[0], s);
+        else
+            count_sort<I, 64>(tokens, n, vocab, keys[0], order[0], s);
+        return hipGetLastError();
+    }
     uint32_t bits = 1;
     while (vocab >> bits)   // keys are 0 .. vocab
         ++bits;
     const uint32_t passes = (bits + kDigitBits - 1) / kDigitBits;
     const uint32_t digit = (bits + passes - 1) / passes;
-    uint32_t *keys[2] = {plan, plan + 2 * (uint64_t)n};
-    uint32_t *order[2] = {plan + n, plan + 3 * (uint64_t)n};
-    if (n <= kSmallSort) {
-        embed_sort_small_kernel<I>
-            <<<1, kSmallThreads, 0, s>>>(tokens, n, vocab, bits, digit, keys[0], order[0]);
-        return hipGetLastError();
-    }
     uint32_t *hist = plan + 4 * (uint64_t)n;
     const uint32_t tiles = (uint32_t)(((uint64_t)n + kSortTile - 1) / kSortTile);
     for (uint32_t p = 0; p < passes; ++p) {
         const uint32_t to = (passes - 1 - p) % 2, from = 1 - to, shift = p * digit;
         if (p == 0)
-            embed_hist_kernel<I, true><<<tiles, kSortThreads, 0, s>>>(
-                tokens, nullptr, n, vocab, shift, digit, hist, tiles);
+            sort_pass<I, true>(tokens, nullptr, nullptr, n, vocab, shift, digit, hist, tiles,
+                               keys[to], order[to], s);
         else
-            embed_hist_kernel<I, false><<<tiles, kSortThreads, 0, s>>>(
-                tokens, keys[from], n, vocab, shift, digit, hist, tiles);
-        embed_scan_kernel<<<1, kScanThreads, 0, s>>>(hist, (uint64_t)tiles << digit, false);
-        if (p == 0)
-            embed_scatter_kernel<I, true><<<tiles, kSortThreads, 0, s>>>(
-                tokens, nullptr, nullptr, n, vocab, shift, digit, hist, tiles, keys[to], order[to]);
-        else
-            embed_scatter_kernel<I, false><<<tiles, kSortThreads, 0, s>>>(
-                tokens, keys[from], order[from], n, vocab, shift, digit, hist, tiles, keys[to],
-                order[to]);
+            sort_pass<I, false>(tokens, keys[from], order[from], n, vocab, shift, digit, hist,
+                                tiles, keys[to], order[to], s);
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess)
             return err;
@@ -610,64 +745,88 @@ hipError_t sort_tokens(const I *tokens, uint32_t n, uint64_t vocab, uint32_t *pl
     return hipSuccess;
 }
 
+template <typename T, Form F>
+void sum_runs(const EmbedGrad &e, uint64_t runs, hipStream_t s)
+{
+    const uint32_t lanes = lanes_for(e.dim, kVec<T>), groups = 256u / lanes;
+    const uint32_t cols = (uint32_t)((e.dim + (uint64_t)lanes * kVec<T> - 1) /
+                                     ((uint64_t)lanes * kVec<T>));
+    const uint64_t blocks = (runs + groups - 1) / groups * cols;
+    const uint64_t zero = F == Form::kWrite ? (e.vocab + kZeroRows - 1) / kZeroRows : 0;
+    embed_grad_kernel<T, F><<<block_grid(blocks + zero), 256, 0, s>>>(e, lanes, cols, blocks);
+}
+
 template <Form F>
 hipError_t grad(const EmbedGrad &e, hipStream_t s)
 {
-    const uint64_t runs = (e.n + kEmbedRun - 1) / kEmbedRun;
-    if (F == Form::kRows && !runs)
-        embed_scan_kernel<<<1, kScanThreads, 0, s>>>((uint32_t *)e.count, 0, true);
-    if constexpr (F == Form::kWrite)
-        embed_zero_kernel<<<block_grid((e.vocab + kWave - 1) / kWave), 256, 0, s>>>(e);
-    if (!runs)
-        return hipGetLastError();
+    const uint64_t runs = (e.n + e.run - 1) / e.run;
+    const uint64_t tiles = (e.n + kEmbedTile - 1) / kEmbedTile;
     if constexpr (F == Form::kRows) {
-        const uint64_t tiles = (e.n + kEmbedTile - 1) / kEmbedTile;
-        embed_starts_kernel<<<(uint32_t)tiles, 256, 0, s>>>(e.keys, (uint32_t)e.n,
-                                                            (uint32_t)e.vocab, e.starts, e.tiles);
-        embed_scan_kernel<<<1, kScanThreads, 0, s>>>(e.tiles, tiles, true);
+        if (runs)
+            embed_starts_kernel<<<(uint32_t)tiles, 256, 0, s>>>(
+                e.keys, (uint32_t)e.n, (uint32_t)e.vocab, e.run, e.starts, e.tiles);
+        embed_scan_kernel<<<1, kScanThreads, 0, s>>>(runs ? e.tiles : (uint32_t *)e.count, tiles);
+        if (!runs)
+            return hipGetLastError();
     }
-    const int vec = e.type == GCQ_F32 ? kVec<float> : kVec<_Float16>;
-    const uint32_t lanes = lanes_for(e.dim, vec), groups = 256u / lanes;
-    const uint64_t cols = (e.dim + (uint64_t)lanes * vec - 1) / ((uint64_t)lanes * vec);
-    const dim3 grid((uint32_t)((runs + groups - 1) / groups), (uint32_t)cols);
     switch (e.type) {
-    case GCQ_F32: embed_grad_kernel<float, F><<<grid, 256, 0, s>>>(e, lanes); break;
-    case GCQ_F16: embed_grad_kernel<_Float16, F><<<grid, 256, 0, s>>>(e, lanes); break;
-    default: embed_grad_kernel<__bf16, F><<<grid, 256, 0, s>>>(e, lanes); break;
+    case GCQ_F32: sum_runs<float, F>(e, runs, s); break;
+    case GCQ_F16: sum_runs<_Float16, F>(e, runs, s); break;
+    default: sum_runs<__bf16, F>(e, runs, s); break;
     }
     if (runs > 1) {
-        const dim3 jgrid((uint32_t)((runs + kJoinRuns - 1) / kJoinRuns),
-                         (uint32_t)((e.dim + 4 * kWave - 1) / (4 * kWave)));
-        embed_join_kernel<F><<<jgrid, kJoinThreads, 0, s>>>(e, (uint32_t)runs);
+        const dim3 grid((uint32_t)((runs + kJoinRuns - 1) / kJoinRuns),
+                        (uint32_t)((e.dim + 4 * kWave - 1) / (4 * kWave)));
+        embed_join_kernel<F><<<grid, kJoinThreads, 0, s>>>(e, runs);
     }
     return hipGetLastError();
 }
 
 uint64_t up256(uint64_t x) { return (x + 255) / 256 * 256; }
 
+// Sorted positions per run: kEmbedRun, or fewer (8 at least) while the runs
+// are too few to give the device 8192 wavefronts of 256 columns.
+uint32_t run_length(uint64_t n, uint64_t dim)
+{
+    uint32_t r = kEmbedRun;
+    while (r > 8 && (n + r - 1) / r * ((dim + 255) / 256) < 8192)
+        r /= 2;
+    return r;
+}
+
+// Where the workspace's parts begin.
+struct WorkLayout {
+    uint64_t tiles, part, bytes;
+};
+
+WorkLayout work_layout(uint64_t n, uint64_t dim)
+{
+    const uint32_t r = run_length(n, dim);
+    const uint64_t runs = (n + r - 1) / r, tiles = (n + kEmbedTile - 1) / kEmbedTile;
+    WorkLayout w;
+    w.tiles = up256(4 * runs);
+    w.part = w.tiles + up256(4 * (tiles + 1));
+    w.bytes = w.part + 8 * runs * dim;
+    return w;
+}
+
 }  // namespace
 
 uint64_t embed_plan_words(uint64_t n)
 {
     const uint64_t tiles = (n + kSortTile - 1) / kSortTile;
-    return 4 * n + (n > kSmallSort ? tiles * kBins : 0);
+    return n <= kCountSort ? 2 * n : 4 * n + (tiles + 1) * kBins;
 }
 
-uint64_t embed_work_bytes(uint64_t n, uint64_t dim)
-{
-    const uint64_t runs = (n + kEmbedRun - 1) / kEmbedRun;
-    const uint64_t tiles = (n + kEmbedTile - 1) / kEmbedTile;
-    return up256(4 * runs) + up256(4 * (tiles + 1)) + 8 * runs * dim;
-}
+uint64_t embed_work_bytes(uint64_t n, uint64_t dim) { return work_layout(n, dim).bytes; }
 
 void embed_work_layout(EmbedGrad &e, void *work)
 {
-    const uint64_t runs = (e.n + kEmbedRun - 1) / kEmbedRun;
-    const uint64_t tiles = (e.n + kEmbedTile - 1) / kEmbedTile;
-    char *p = (char *)work;
-    e.starts = (uint32_t *)p;
-    e.tiles = (uint32_t *)(p + up256(4 * runs));
-    e.part = (float *)(p + up256(4 * runs) + up256(4 * (tiles + 1)));
+    const WorkLayout w = work_layout(e.n, e.dim);
+    e.run = run_length(e.n, e.dim);
+    e.starts = (uint32_t *)work;
+    e.tiles = (uint32_t *)((char *)work + w.tiles);
+    e.part = (float *)((char *)work + w.part);
 }
 
 hipError_t launch_embed_lookup(const EmbedTable &t, const void *tokens, bool tok64, uint64_t n,

@@ -101,8 +101,8 @@ __device__ __forceinline__ uint64_t block_number()
 }  // namespace lm
 
 // ---- embedding ----------------------------------------------------------
-// Sorted positions are summed in runs of kEmbedRun; a run's open ends leave
-// partial sums in the workspace.
+// Sorted positions are summed in runs of at most kEmbedRun; a run's open ends
+// leave partial sums in the workspace.
 constexpr uint32_t kEmbedRun = 32;
 // Positions per entry of the segment counts.
 constexpr uint32_t kEmbedTile = 1024;
@@ -124,6 +124,7 @@ struct EmbedGrad {
     uint64_t out_ld;
     int32_t *ids, *count;           // row-sparse form (null: dense)
     bool add;                       // dense: add to out; else overwrite
+    uint32_t run;                   // sorted positions per run
     uint32_t *starts;               // workspace: segment starts before each run, in its tile
     uint32_t *tiles;                // workspace: segment starts before each tile, then all
     float *part;                    // workspace: [runs][2][dim] open sums
@@ -131,7 +132,7 @@ struct EmbedGrad {
 
 uint64_t embed_plan_words(uint64_t n);
 uint64_t embed_work_bytes(uint64_t n, uint64_t dim);
-// Fills in the workspace pointers of `e`.
+// Fills in the run length and the workspace pointers of `e`.
 void embed_work_layout(EmbedGrad &e, void *work);
 hipError_t launch_embed_lookup(const EmbedTable &t, const void *tokens, bool tok64, uint64_t n,
                                float scale, void *out, int out_type, uint64_t out_ld,

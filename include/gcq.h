@@ -493,8 +493,8 @@ int embed_sort(const void *tokens, int token_type, size_t n, size_t vocab, uint3
  * zero.  Otherwise dtable += d, and rows that no token names are left as they
  * are (gradients of several passes, or of a table tied to the output
  * projection).  Positions of one token are summed in ascending order within
- * runs of 32 sorted positions and the runs' sums in a fixed order.  Rows of
- * grad at padding are not read.
+ * runs of sorted positions (8 to 32, by n and dim) and the runs' sums in a
+ * fixed order.  Rows of grad at padding are not read.
  *
  *   grad    in,     n x dim of grad_type (a float type), rows grad_ld apart
  *   plan    in,     from embed_sort with this n and vocab

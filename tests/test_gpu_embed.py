@@ -91,6 +91,7 @@ def test_lookup_keeps_special_values(gpu):
 
 
 @pytest.mark.parametrize("n,vocab", [(1, 1), (2, 2 ** 31 - 1), (65, 3), (4096, 600), (4097, 600),
+                                     (8193, 50000), (16384, 131072), (16385, 131072),
                                      (5000, 40), (20000, 131073), (70001, 2 ** 20 + 1),
                                      (9000, 2 ** 31 - 1), (300000, 70000)])
 @pytest.mark.parametrize("index", ["int32", "int64"])
@@ -146,6 +147,33 @@ def test_gradient(gpu, kind, grad_type):
         assert u == named.size and np.array_equal(ids[:u].cpu().numpy(), named)
         assert torch.equal(rows[:u], out[torch.from_numpy(named).cuda()])
         assert (ids[u:] == -9).all() and (rows[u:] == 7.0).all()
+
+
+@pytest.mark.parametrize("n,vocab,dim", [(40000, 3000, 1024), (70001, 20000, 1030)])
+def test_gradient_of_many(gpu, n, vocab, dim):
+    """Long runs and segments of thousands of positions; the reference sums in
+    64 bits on the GPU."""
+    import torch
+
+    rs = np.random.default_rng(7)
+    tok = tokens_of(rs, n, vocab, "text")
+    g = grads(rs, n, dim, torch.bfloat16)
+    ok = torch.from_numpy((tok >= 0) & (tok < vocab)).cuda()
+    at = torch.where(ok, torch.from_numpy(tok).cuda(), 0)
+    gd = torch.where(ok[:, None], g.double(), 0.0)
+    want = torch.zeros(vocab, dim, dtype=torch.float64, device="cuda").index_add_(0, at, gd)
+    mag = torch.zeros_like(want).index_add_(0, at, gd.abs())
+    count = torch.zeros(vocab, dtype=torch.float64, device="cuda").index_add_(0, at, ok.double())
+    plan = gpu.embed_sort(torch.from_numpy(tok).cuda(), vocab)
+    out = gpu.embed_grad(g, plan)
+    assert ((out.double() - want).abs() <= (count[:, None] + 2) * 2.0 ** -24 * mag).all()
+    ids, rows, cnt = gpu.embed_grad_rows(g, plan)
+    named = torch.nonzero(count)[:, 0]
+    assert int(cnt) == named.numel() and torch.equal(ids[:int(cnt)].long(), named)
+    assert torch.equal(rows[:int(cnt)], out[named])
+    base = torch.ones(vocab, dim, device="cuda")
+    acc = gpu.embed_grad(g, plan, out=base.clone(), accumulate=True)
+    assert torch.equal(acc, out + 1.0)
 
 
 def test_gradient_of_nothing(gpu):
