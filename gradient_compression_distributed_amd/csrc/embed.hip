@@ -21,8 +21,13 @@ using namespace lm;
 
 // ------------------------------------------------------------------ lookup
 // L lanes share a row (a power of two up to 256), so a workgroup of 256
-// threads copies 256 / L rows at once; a lane strides over its row.
-template <typename T, typename O, typename I>
+// threads copies 256 / L rows at once, R times over.  The R tokens are loaded
+// together and then the R rows' vectors, so a row waits for one load, not for
+// two in turn.
+template <typename T, typename O>
+constexpr int kLookup = kVec<T> < kVec<O> ? kVec<T> : kVec<O>;   // 16 bytes at most on either side
+
+template <typename T, typename O, typename I, int R>
 __global__ __launch_bounds__(256) void embed_lookup_kernel(const T *__restrict__ table,
                                                            uint64_t vocab, uint64_t dim,
                                                            uint64_t ld,
@@ -31,22 +36,33 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(const T *__restrict__
                                                            O *__restrict__ out, uint64_t out_ld,
                                                            uint32_t lanes)
 {
-    constexpr int N = kVec<T>;
-    const uint32_t lane = threadIdx.x & (lanes - 1), slot = threadIdx.x / lanes;
-    const uint64_t row = block_number() * (256u / lanes) + slot;
-    if (row >= n)
-        return;
-    const uint64_t tok = (uint64_t)(int64_t)((const GCQ_G I *)tokens)[row];
-    const bool real = tok < vocab;   // a negative token is past any vocab
-    const T *src = table + (real ? tok : 0) * ld;
-    O *dst = out + row * out_ld;
-#pragma unroll 2
+    constexpr int N = kLookup<T, O>;
+    const uint32_t lane = threadIdx.x & (lanes - 1), slots = 256u / lanes;
+    const uint64_t row0 = block_number() * slots * R + threadIdx.x / lanes;   // then every slots-th
+    uint64_t tok[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint64_t row = row0 + (uint64_t)r * slots;
+        tok[r] = row < n ? (uint64_t)(int64_t)((const GCQ_G I *)tokens)[row] : ~0ull;
+    }
     for (uint64_t c = (uint64_t)lane * N; c < dim; c += (uint64_t)lanes * N) {
         const int64_t left = (int64_t)(dim - c);
-        fvec<N> f = 0.0f;
-        if (real)
-            f = to_f32<T, N>(load_vec<T, N>(src + c, left)) * scale;
-        store_vec<O, N>(dst + c, from_f32<O, N>(f), left);
+        vec<T, N> v[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            v[r] = (T)0.0f;
+            if (tok[r] < vocab)   // a negative token is past any vocab
+                v[r] = load_vec<T, N>(table + tok[r] * ld + c, left);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint64_t row = row0 + (uint64_t)r * slots;
+            fvec<N> f = 0.0f;
+            if (tok[r] < vocab)
+                f = to_f32<T, N>(v[r]) * scale;   // a padding row stays +0
+            if (row < n)
+                store_vec<O, N, true>(out + row * out_ld + c, from_f32<O, N>(f), left);
+        }
     }
 }
 
@@ -63,7 +79,7 @@ __device__ __forceinline__ uint32_t key_of(int64_t token, uint64_t vocab)
 // take a position each, 1024 / Ti groups of lanes a share of the others.
 // n^2 comparisons (2 instructions each) cost less than the passes of a radix
 // sort, each of them bound by launch and latency, up to kCountSort positions.
-constexpr uint32_t kCountSort = 16384;
+constexpr uint32_t kCountSort = 8192;
 template <typename I, uint32_t Ti>
 __global__ __launch_bounds__(1024) void embed_count_sort_kernel(const I *__restrict__ tokens,
                                                                 uint32_t n, uint32_t share,
@@ -320,6 +336,9 @@ __global__ __launch_bounds__(kSortThreads) void embed_scatter_kernel(
 }
 
 // ---------------------------------------------------------------- gradient
+// Up to here one workgroup counts the segment starts (8 positions a thread,
+// the shortest run), beyond it a launch per tile and a scan.
+constexpr uint32_t kSmallStarts = 8192;
 // Segment starts before each run of sorted positions (within its tile), and
 // each tile's count.
 __global__ __launch_bounds__(256) void embed_starts_kernel(const uint32_t *__restrict__ keys,
@@ -346,6 +365,33 @@ __global__ __launch_bounds__(256) void embed_starts_kernel(const uint32_t *__res
         starts[i0 / run] = before;
     if (threadIdx.x == 0)
         tiles[blockIdx.x] = total;
+}
+
+// Both at once by one workgroup: the starts counted from the first position,
+// the tiles' counts 0 but for the total.
+__global__ __launch_bounds__(1024) void embed_starts_small_kernel(const uint32_t *__restrict__ keys,
+                                                                  uint32_t n, uint32_t vocab,
+                                                                  uint32_t run,
+                                                                  uint32_t *__restrict__ starts,
+                                                                  uint32_t *__restrict__ tiles)
+{
+    __shared__ uint32_t sums[1024 / kWave];
+    constexpr uint32_t per = kSmallStarts / 1024u;
+    const uint32_t i0 = threadIdx.x * per;
+    uint32_t k[per + 1], mine = 0;
+#pragma unroll
+    for (uint32_t j = 0; j <= per; ++j)   // k[j]: the key before position i0 + j
+        k[j] = i0 + j >= 1 && i0 + j <= n ? keys[i0 + j - 1] : 0xFFFFFFFFu;
+#pragma unroll
+    for (uint32_t j = 0; j < per; ++j)
+        mine += k[j + 1] != k[j] && k[j + 1] < vocab;
+    uint32_t total;
+    const uint32_t before = block_scan<1024>(mine, sums, total);
+    if (i0 < n && i0 % run == 0)
+        starts[i0 / run] = before;
+    const uint32_t count = (n + kEmbedTile - 1) / kEmbedTile;
+    if (threadIdx.x <= count)
+        tiles[threadIdx.x] = threadIdx.x < count ? 0u : total;
 }
 
 // In-place exclusive scan of a[0..m) by one workgroup, the total to a[m].
@@ -378,17 +424,33 @@ __global__ __launch_bounds__(kScanThreads) void embed_scan_kernel(uint32_t *__re
 
 enum class Form { kWrite, kAdd, kRows };
 
-// Zeroes the rows [v0, v0 + 64) of the dense gradient that no position names.
-// 128 threads each search for the first position of a row >= v0 and of one
-// >= v0 + 64, a 128th of the range at a time; the positions between name the
-// rows to leave.
-constexpr uint32_t kZeroRows = 64;
-__device__ __forceinline__ void zero_rows(const EmbedGrad &e, uint64_t v0)
+// p[0..count) = 0 by 256 threads, in aligned vectors but for the ends.
+__device__ __forceinline__ void zero_floats(float *p, uint64_t count)
+{
+    GCQ_G float *q = (GCQ_G float *)p;
+    const uint32_t tid = threadIdx.x;
+    const uint64_t skip = (4u - ((uintptr_t)p / 4u) % 4u) % 4u, head = skip < count ? skip : count;
+    if (tid < head)
+        q[tid] = 0.0f;
+    const uint64_t body = (count - head) / 4u;
+    const dev::v4f zero = 0.0f;
+    for (uint64_t i = tid; i < body; i += 256u)
+        ((GCQ_G dev::v4f *)(q + head))[i] = zero;
+    const uint64_t at = head + 4u * body + tid;
+    if (at < count)
+        q[at] = 0.0f;
+}
+
+// Zeroes the rows [v0, v0 + span) of the dense gradient that no position
+// names, span <= 64.  128 threads each search for the first position of a row
+// >= v0 and of one >= v0 + span, a 128th of the range at a time; the
+// positions between name the rows to leave.
+__device__ __forceinline__ void zero_rows(const EmbedGrad &e, uint64_t v0, uint32_t span)
 {
     __shared__ uint32_t votes[4];
     __shared__ unsigned long long named;
     const uint32_t tid = threadIdx.x, side = tid / 128u;
-    const uint64_t target = v0 + (side ? kZeroRows : 0u);
+    const uint64_t target = v0 + (side ? span : 0u);
     uint64_t lo[2] = {0, 0}, hi[2] = {e.n, e.n};
     if (tid == 0)
         named = 0;
@@ -419,7 +481,7 @@ __device__ __forceinline__ void zero_rows(const EmbedGrad &e, uint64_t v0)
             mine |= 1ull << (e.keys[i] - v0);
         if (mine)
             atomicOr(&named, (unsigned long long)mine);
-    } else if (tid < kZeroRows) {   // long segments: each row looks for its first position
+    } else if (tid < kWave) {   // long segments: each row looks for its first position
         uint64_t l = a, h = b;
         while (l < h) {
             const uint64_t mid = (l + h) / 2;
@@ -433,15 +495,18 @@ __device__ __forceinline__ void zero_rows(const EmbedGrad &e, uint64_t v0)
             named = m;
     }
     __syncthreads();
-    const uint64_t rows = e.vocab - v0 < kZeroRows ? e.vocab - v0 : kZeroRows;
+    const uint64_t rows = e.vocab - v0 < span ? e.vocab - v0 : span;
     uint64_t m = ~(uint64_t)named;
     if (rows < 64)
         m &= (1ull << rows) - 1u;
-    const vec<float, 4> zero = 0.0f;
-    for (; m; m &= m - 1) {
-        float *row = e.out + (v0 + (uint64_t)__builtin_ctzll(m)) * e.out_ld;
-        for (uint64_t c = tid * 4u; c < e.dim; c += 1024u)
-            store_vec<float, 4>(row + c, zero, (int64_t)(e.dim - c));
+    // neighbouring rows without a gap are one stretch
+    const bool dense = e.out_ld == e.dim;
+    while (m) {
+        const uint32_t r = (uint32_t)__builtin_ctzll(m);
+        const uint64_t rest = ~(m >> r);
+        const uint32_t count = !dense ? 1u : rest ? (uint32_t)__builtin_ctzll(rest) : 64u - r;
+        zero_floats(e.out + (v0 + r) * e.out_ld, count * e.dim);
+        m &= count + r >= 64 ? 0ull : ~0ull << (r + count);
     }
 }
 
@@ -453,7 +518,7 @@ __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64
     fvec<N> v = acc * e.scale;
     if constexpr (F == Form::kAdd)
         v += old;
-    store_vec<float, N>(e.out + row * e.out_ld + c, v, left);
+    store_vec<float, N, true>(e.out + row * e.out_ld + c, v, left);
 }
 
 // One pass over g in sorted order.  L lanes (a power of two up to 256) share
@@ -463,15 +528,15 @@ __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64
 // workgroups behind the first `blocks` zero the rows that no position names.
 template <typename T, Form F>
 __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t lanes, uint32_t cols,
-                                                         uint64_t blocks)
+                                                         uint64_t blocks, uint32_t span)
 {
-    constexpr int N = kVec<T>, U = 4;
+    constexpr int N = 4, U = F == Form::kAdd ? 4 : 8;
     const uint64_t block = block_number();
     if constexpr (F == Form::kWrite) {
         if (block >= blocks) {
-            const uint64_t v0 = (block - blocks) * kZeroRows;
+            const uint64_t v0 = (block - blocks) * span;
             if (v0 < e.vocab)
-                zero_rows(e, v0);
+                zero_rows(e, v0, span);
             return;
         }
     }
@@ -513,10 +578,10 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t l
             old[j] = 0.0f;
             if (i < len && key[i] < e.vocab) {
                 if (pos[i] < n)
-                    v[j] = load_vec<T, N>(g + pos[i] * e.ld, left);
+                    v[j] = load_vec<T, N, true>(g + pos[i] * e.ld, left);
                 if constexpr (F == Form::kAdd)
                     if (key[i] != key[i + 1])
-                        old[j] = load_vec<float, N>(e.out + key[i] * e.out_ld + c, left);
+                        old[j] = load_vec<float, N, true>(e.out + key[i] * e.out_ld + c, left);
             }
         }
 #pragma unroll
@@ -560,7 +625,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t l
 // runs and 256 columns; a wavefront adds up a segment of at most kJoinShort
 // parts by itself, longer ones are shared by all 8 (consecutive parts each,
 // their sums added in order).
-constexpr uint32_t kJoinThreads = 512, kJoinRuns = 16, kJoinShort = 16;
+constexpr uint32_t kJoinThreads = 512, kJoinRuns = 8, kJoinShort = 16, kJoinBatch = 8;
 template <Form F>
 __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, uint64_t runs)
 {
@@ -571,38 +636,60 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, u
     const uint64_t c = ((uint64_t)blockIdx.y * kWave + lane) * N;
     const int64_t left = c < e.dim ? (int64_t)(e.dim - c) : 0;
     const uint64_t run0 = (uint64_t)blockIdx.x * kJoinRuns;
-    // every wavefront: which of the runs begin a segment that reaches over
-    // their end, and with which key
-    bool joins = false;
-    uint32_t k0 = 0;
+    // every wavefront: lane l holds the last key of run run0 + l and the first
+    // key of the one behind it, and whether the run begins a segment that
+    // reaches over its end
+    uint32_t k0 = 0xFFFFFFFFu, next = 0xFFFFFFFFu, prev = 0xFFFFFFFFu;
     {
-        const uint64_t end = (run0 + lane + 1) * R;
-        if (lane < kJoinRuns && end < e.n) {
+        const uint64_t i0 = (run0 + lane) * R, end = i0 + R;
+        if (end < e.n) {
             k0 = e.keys[end - 1];
-            const uint64_t i0 = end - R;
-            const uint32_t next = e.keys[end], prev = i0 ? e.keys[i0 - 1] : 0xFFFFFFFFu;
-            joins = k0 < e.vocab && next == k0 && prev != k0;
+            next = e.keys[end];
+            if (i0)
+                prev = e.keys[i0 - 1];
         }
     }
+    const bool joins = lane < kJoinRuns && k0 < e.vocab && next == k0 && prev != k0;
     uint32_t turn = 0;
     for (uint64_t m = __ballot(joins); m; m &= m - 1, ++turn) {
         const uint32_t q = (uint32_t)__builtin_ctzll(m);
         const uint32_t k = (uint32_t)__shfl((int)k0, (int)q, kWave);
         const uint64_t run = run0 + q;
-        // the following runs that it opens: 64 at a time
-        uint64_t parts = 1;
-        for (;;) {
-            const uint64_t at = (run + parts + lane) * R;
-            const uint64_t goes = __ballot(at < e.n && e.keys[at] == k);
-            const uint32_t more = ~goes ? (uint32_t)__builtin_ctzll(~goes) : 64u;
-            parts += more;
-            if (more < 64)
-                break;
+        // this run and the following ones that begin with k
+        const uint64_t stops = ~(__ballot(next == k) >> q);
+        uint64_t parts = 1 + (stops ? (uint32_t)__builtin_ctzll(stops) : 64u);
+        if (parts == 65 - q) {   // no lane ends it: look at the next 64 runs, and so on
+            for (;;) {
+                const uint64_t at = (run + parts + lane) * R;
+                const uint64_t goes = ~__ballot(at < e.n && e.keys[at] == k);
+                parts += goes ? (uint32_t)__builtin_ctzll(goes) : 64u;
+                if (goes)
+                    break;
+            }
         }
         const bool alone = parts <= kJoinShort;
         if (alone && turn % waves != wave)
             continue;
         fvec<N> old = 0.0f;
+        if constexpr (F == Form::kAdd)
+            if (left > 0)
+                old = load_vec<float, N>(e.out + (uint64_t)k * e.out_ld + c, left);
+        const uint64_t each = alone ? parts : (parts + waves - 1) / waves;
+        const uint64_t p0 = alone ? 0 : wave * each, p1 = p0 + each < parts ? p0 + each : parts;
+        fvec<N> acc = 0.0f;
+        for (uint64_t p = p0; p < p1; p += kJoinBatch) {
+            vec<float, N> v[kJoinBatch];
+#pragma unroll
+            for (uint32_t u = 0; u < kJoinBatch; ++u) {
+                v[u] = 0.0f;
+                if (p + u < p1 && left > 0)
+                    v[u] = load_vec<float, N>(
+                        e.part + (2 * (run + p + u) + (p + u ? 0 : 1)) * e.dim + c, left);
+            }
+#pragma unroll
+            for (uint32_t u = 0; u < kJoinBatch; ++u)
+                acc += v[u];
+        }
         uint64_t row = k;
         if constexpr (F == Form::kRows) {
             // the last segment that opens in this run
@@ -613,17 +700,6 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, u
             }
             row = (uint64_t)e.tiles[run * R / kEmbedTile] + e.starts[run] +
                   (uint32_t)__popcll(__ballot(opens)) - 1u;
-        }
-        if constexpr (F == Form::kAdd)
-            if (left > 0)
-                old = load_vec<float, N>(e.out + row * e.out_ld + c, left);
-        const uint64_t each = alone ? parts : (parts + waves - 1) / waves;
-        const uint64_t p0 = alone ? 0 : wave * each, p1 = p0 + each < parts ? p0 + each : parts;
-        fvec<N> acc = 0.0f;
-        if (left > 0) {
-#pragma unroll 8
-            for (uint64_t p = p0; p < p1; ++p)
-                acc += load_vec<float, N>(e.part + (2 * (run + p) + (p ? 0 : 1)) * e.dim + c, left);
         }
         if (alone) {
             if (left > 0)
@@ -654,10 +730,14 @@ template <typename T, typename O, typename I>
 hipError_t lookup(const EmbedTable &t, const void *tokens, uint64_t n, float scale, void *out,
                   uint64_t out_ld, hipStream_t s)
 {
-    const uint32_t lanes = lanes_for(t.dim, kVec<T>);
-    const uint64_t per = 256u / lanes;
-    embed_lookup_kernel<T, O, I><<<block_grid((n + per - 1) / per), 256, 0, s>>>(
-        (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
+    const uint32_t lanes = lanes_for(t.dim, kLookup<T, O>);
+    const uint64_t per = 256u / lanes, blocks = (n + per - 1) / per;
+    if (blocks >= 4096)
+        embed_lookup_kernel<T, O, I, 2><<<block_grid((blocks + 1) / 2), 256, 0, s>>>(
+            (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
+    else
+        embed_lookup_kernel<T, O, I, 1><<<block_grid(blocks), 256, 0, s>>>(
+            (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
     return hipGetLastError();
 }
 
@@ -714,13 +794,11 @@ hipError_t sort_tokens(const I *tokens, uint32_t n, uint64_t vocab, uint32_t *pl
 {
     uint32_t *keys[2] = {plan, plan + 2 * (uint64_t)n};
     uint32_t *order[2] = {plan + n, plan + 3 * (uint64_t)n};
-    if (n <= kCountSort) {   // 256 workgroups or more where the positions allow it
+    if (n <= kCountSort) {   // a workgroup per CU
         if (n <= 4096)
             count_sort<I, 16>(tokens, n, vocab, keys[0], order[0], s);
-        else if (n <= 8192)
-            count_sort<I, 32>(tokens, n, vocab, keys[0], order[0], s);
         else
-            count_sort<I, 64>(tokens, n, vocab, keys[0], order[0], s);
+            count_sort<I, 32>(tokens, n, vocab, keys[0], order[0], s);
         return hipGetLastError();
     }
     uint32_t bits = 1;
@@ -748,12 +826,13 @@ hipError_t sort_tokens(const I *tokens, uint32_t n, uint64_t vocab, uint32_t *pl
 template <typename T, Form F>
 void sum_runs(const EmbedGrad &e, uint64_t runs, hipStream_t s)
 {
-    const uint32_t lanes = lanes_for(e.dim, kVec<T>), groups = 256u / lanes;
-    const uint32_t cols = (uint32_t)((e.dim + (uint64_t)lanes * kVec<T> - 1) /
-                                     ((uint64_t)lanes * kVec<T>));
+    const uint32_t lanes = lanes_for(e.dim, 4), groups = 256u / lanes;
+    const uint32_t cols = (uint32_t)((e.dim + 4ull * lanes - 1) / (4ull * lanes));
     const uint64_t blocks = (runs + groups - 1) / groups * cols;
-    const uint64_t zero = F == Form::kWrite ? (e.vocab + kZeroRows - 1) / kZeroRows : 0;
-    embed_grad_kernel<T, F><<<block_grid(blocks + zero), 256, 0, s>>>(e, lanes, cols, blocks);
+    // rows that a zeroing workgroup looks at: about 64 KiB, 64 at most
+    const uint32_t span = (uint32_t)(e.dim >= 16384 ? 1u : e.dim <= 256 ? 64u : 16384 / e.dim);
+    const uint64_t zero = F == Form::kWrite ? (e.vocab + span - 1) / span : 0;
+    embed_grad_kernel<T, F><<<block_grid(blocks + zero), 256, 0, s>>>(e, lanes, cols, blocks, span);
 }
 
 template <Form F>
@@ -762,10 +841,15 @@ hipError_t grad(const EmbedGrad &e, hipStream_t s)
     const uint64_t runs = (e.n + e.run - 1) / e.run;
     const uint64_t tiles = (e.n + kEmbedTile - 1) / kEmbedTile;
     if constexpr (F == Form::kRows) {
-        if (runs)
-            embed_starts_kernel<<<(uint32_t)tiles, 256, 0, s>>>(
-                e.keys, (uint32_t)e.n, (uint32_t)e.vocab, e.run, e.starts, e.tiles);
-        embed_scan_kernel<<<1, kScanThreads, 0, s>>>(runs ? e.tiles : (uint32_t *)e.count, tiles);
+        if (runs && e.n <= kSmallStarts) {
+            embed_starts_small_kernel<<<1, 1024, 0, s>>>(e.keys, (uint32_t)e.n, (uint32_t)e.vocab,
+                                                         e.run, e.starts, e.tiles);
+        } else {
+            if (runs)
+                embed_starts_kernel<<<(uint32_t)tiles, 256, 0, s>>>(
+                    e.keys, (uint32_t)e.n, (uint32_t)e.vocab, e.run, e.starts, e.tiles);
+            embed_scan_kernel<<<1, kScanThreads, 0, s>>>(runs ? e.tiles : (uint32_t *)e.count, tiles);
+        }
         if (!runs)
             return hipGetLastError();
     }

@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "gcq_device.h"
 #include "gcq_internal.h"
 
 namespace gcq {
@@ -29,11 +30,12 @@ using fvec = float __attribute__((ext_vector_type(N)));
 #define GCQ_G __attribute__((address_space(1)))
 
 // v[0..N) = p[0..N), or only the first `left` of them (the rest 0).
-template <typename T, int N>
+// Nt: non-temporal, for what no other workgroup reads.
+template <typename T, int N, bool Nt = false>
 __device__ __forceinline__ vec<T, N> load_vec(const T *p, int64_t left)
 {
     if (left >= N)
-        return *(const GCQ_G vec<T, N> *)p;
+        return dev::ld<Nt>((const GCQ_G vec<T, N> *)p);
     vec<T, N> v;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -41,11 +43,11 @@ __device__ __forceinline__ vec<T, N> load_vec(const T *p, int64_t left)
     return v;
 }
 
-template <typename T, int N>
+template <typename T, int N, bool Nt = false>
 __device__ __forceinline__ void store_vec(T *p, vec<T, N> v, int64_t left)
 {
     if (left >= N) {
-        *(GCQ_G vec<T, N> *)p = v;
+        dev::st<Nt>((GCQ_G vec<T, N> *)p, v);
         return;
     }
 #pragma unroll
