@@ -559,17 +559,29 @@ def qsgd_elias_decode(words, offsets, n: int, d: int, norms=None, nibbles=None):
 # Matrices are 2-D tensors whose rows are contiguous; rows may lie further
 # apart than their length (a slice of columns).  A call runs on the device of
 # its tensors, on that device's current stream, whatever device is current.
-_type_codes = None
+# What a call needs of torch, looked up once (by _lm): the small calls take a
+# few microseconds, and an import statement or a Stream object is a part of it.
+_torch = _type_codes = _raw_stream = _current_device = None
+
+
+def _lm():
+    """The library, with the names above set."""
+    global _torch, _type_codes, _raw_stream, _current_device
+    if _torch is None:
+        import torch
+
+        load()
+        _type_codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int32: 3,
+                       torch.int64: 4}
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _torch = torch
+    return _lib if _lib is not None else load()
 
 
 def _type_code(x, name, allowed=(0, 1, 2)):
     """The C ABI's enum gcq_type of a tensor's element type."""
-    global _type_codes
-    if _type_codes is None:
-        import torch
-
-        _type_codes = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.int32: 3,
-                       torch.int64: 4}
     code = _type_codes.get(x.dtype, -1)
     if code not in allowed:
         raise TypeError(f"{name} has type {x.dtype}, which this call does not take")
@@ -622,14 +634,11 @@ def _vector(x, name, n, device, dtype=None, at_least=False):
 def _call(fn, where, device, *args):
     """fn(*args, stream) on a device's current stream, with that device
     current while it runs."""
-    import torch
-
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device:
-        status = fn(*args, stream)
+    if _current_device() == device:
+        status = fn(*args, _raw_stream(device))
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, stream)
+        with _torch.cuda.device(device):
+            status = fn(*args, _raw_stream(device))
     if status != 0:
         raise GcqError(status, where)
 
@@ -645,9 +654,7 @@ def embed_work_bytes(n: int, dim: int) -> int:
 def embed_lookup(table, tokens, scale: float = 1.0, out=None):
     """out[i] = scale * table[tokens[i]], rounded once to out's type (the
     table's by default).  Tokens outside the table are padding: zero rows."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     dev = _on(table, "table")
     if table.dim() != 2:
         raise ValueError("table must be a matrix")
@@ -675,9 +682,7 @@ class EmbedPlan:
 def embed_sort(tokens, vocab: int, plan=None) -> EmbedPlan:
     """The plan of a batch's tokens for embed_grad and embed_grad_rows.  A
     plan of as many tokens is overwritten if given."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     n = tokens.numel()
     dev = _on(tokens, "tokens")
     _vector(tokens, "tokens", n, dev)
@@ -694,8 +699,7 @@ def embed_sort(tokens, vocab: int, plan=None) -> EmbedPlan:
 
 
 def _embed_grad_args(lib, grad, plan, dim, work):
-    import torch
-
+    torch = _torch
     dev = _on(grad, "grad")
     ld = _matrix(grad, "grad", plan.n, dim, dev)
     _vector(plan.words, "plan", lib.embed_plan_words(plan.n), dev, torch.int32, at_least=True)
@@ -712,9 +716,7 @@ def embed_grad(grad, plan: EmbedPlan, scale: float = 1.0, out=None, accumulate: 
     """The table's gradient, float32: out[v] = scale * (sum of grad[i] over
     the positions i of token v), zero where no token is; with ``accumulate``
     it is added to out instead."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     dim = grad.shape[-1]
     dev, ld, work = _embed_grad_args(lib, grad, plan, dim, work)
     if out is None:
@@ -735,9 +737,7 @@ def embed_grad_rows(grad, plan: EmbedPlan, scale: float = 1.0, ids=None, rows=No
     int32[1]).  The first ``count`` ids are the batch's different tokens in
     ascending order and the same rows their gradients; what is behind them is
     left as it was.  ids and rows hold at least min(n, vocab) entries."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     dim = grad.shape[-1]
     dev, ld, work = _embed_grad_args(lib, grad, plan, dim, work)
     most = min(plan.n, plan.vocab)
@@ -758,17 +758,14 @@ def embed_grad_rows(grad, plan: EmbedPlan, scale: float = 1.0, ids=None, rows=No
 
 
 def rms_norm_work_bytes(rows: int, dim: int, dtype) -> int:
-    import torch
-
-    return int(load().rms_norm_work_bytes(rows, dim, _type_code(torch.empty(0, dtype=dtype), "dtype")))
+    return int(_lm().rms_norm_work_bytes(rows, dim, _type_codes.get(dtype, -1)))
 
 
 def _rms_args(x, weight, residual, h, rstd):
     """The checks rms_norm and rms_norm_q8 share; (device, rows, dim, type,
     arguments of x and the residual, arguments of the weight, h, its
     arguments, rstd)."""
-    import torch
-
+    torch = _torch
     dev = _on(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
@@ -800,9 +797,7 @@ def rms_norm(x, weight, eps: float, residual=None, y=None, h=None, rstd=None):
     rstd).  h is the sum, rounded to x's type (x itself without a residual;
     it may be given as the residual, which is then updated), rstd what
     rms_norm_grad needs."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     dev, rows, dim, kind, args, h, tail, rstd = _rms_args(x, weight, residual, h, rstd)
     if y is None:
         y = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
@@ -817,9 +812,7 @@ def rms_norm_q8(x, weight, eps: float, group: int = 128, residual=None, codes=No
     """rms_norm with y as e4m3 codes (torch.float8_e4m3fn) and a float32 scale
     per group of 32, 64 or 128 columns (group 0: per row): y is about code *
     scale.  Returns (codes, scales [rows, groups], h, rstd)."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     dev, rows, dim, _, args, h, tail, rstd = _rms_args(x, weight, residual, h, rstd)
     if group not in (0, 32, 64, 128):
         raise ValueError(f"group must be 0, 32, 64 or 128 (got {group})")
@@ -843,9 +836,7 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, accumulat
     otherwise): returns (dx, dweight).  dx is the gradient of x and of the
     residual; it may be given as dh.  dweight is float32; with ``accumulate``
     it is added to."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     dev = _on(dy, "dy")
     if dy.dim() != 2:
         raise ValueError("dy must be a matrix")
@@ -893,9 +884,7 @@ def _distill_args(logits, index, teacher, temperature, row_scale, scale):
     idx_ld = _matrix(index, "index", rows, k, dev)
     top_ld = _matrix(teacher, "teacher", rows, k, dev)
     if row_scale is not None:
-        import torch
-
-        _vector(row_scale, "row_scale", rows, dev, torch.float32)
+        _vector(row_scale, "row_scale", rows, dev, _torch.float32)
     return (dev, rows, vocab, kind, (logits.data_ptr(), kind, rows, vocab, ld),
             (index.data_ptr(), _type_code(index, "index", (3, 4)), idx_ld, teacher.data_ptr(),
              _type_code(teacher, "teacher", (kind, 0)), top_ld, k, temperature,
@@ -904,8 +893,7 @@ def _distill_args(logits, index, teacher, temperature, row_scale, scale):
 
 def _row_floats(x, name, rows, dev, like):
     """A float32 vector of a value per row, new if none is given."""
-    import torch
-
+    torch = _torch
     if x is None:
         return torch.empty(rows, dtype=torch.float32, device=like.device)
     _vector(x, name, rows, dev, torch.float32)
@@ -913,8 +901,7 @@ def _row_floats(x, name, rows, dev, like):
 
 
 def _dlogits(out, logits, rows, vocab, kind, dev):
-    import torch
-
+    torch = _torch
     if out is None:
         out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
     _type_code(out, "out", (kind,))
@@ -929,7 +916,7 @@ def distill_loss(logits, index, teacher, temperature: float = 1.0, row_scale=Non
     loss = s * KL(softmax(teacher / T) || softmax(logits / T)), the student's
     softmax over the whole vocabulary, s = scale * row_scale; rows with s = 0
     are not read."""
-    lib = load()
+    lib = _lm()
     dev, rows, _, _, head, tail = _distill_args(logits, index, teacher, temperature, row_scale, scale)
     loss = _row_floats(loss, "loss", rows, dev, logits)
     lse = _row_floats(lse, "lse", rows, dev, logits)
@@ -941,9 +928,7 @@ def distill_grad(logits, lse, index, teacher, temperature: float = 1.0, row_scal
                  scale: float = 1.0, out=None):
     """The gradient of sum(loss) in the logits, from distill_loss's lse;
     ``row_scale`` may carry the gradient from above.  out may be the logits."""
-    import torch
-
-    lib = load()
+    lib, torch = _lm(), _torch
     dev, rows, vocab, kind, head, tail = _distill_args(logits, index, teacher, temperature, row_scale,
                                                        scale)
     _vector(lse, "lse", rows, dev, torch.float32)
@@ -956,7 +941,7 @@ def distill_loss_grad(logits, index, teacher, temperature: float = 1.0, row_scal
                       scale: float = 1.0, loss=None, lse=None, out=None):
     """distill_loss and distill_grad in one launch: (loss, lse, dlogits).  out
     may be the logits, which it then replaces."""
-    lib = load()
+    lib = _lm()
     dev, rows, vocab, kind, head, tail = _distill_args(logits, index, teacher, temperature, row_scale,
                                                        scale)
     loss = _row_floats(loss, "loss", rows, dev, logits)

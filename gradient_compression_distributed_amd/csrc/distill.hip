@@ -39,6 +39,16 @@ __device__ __forceinline__ Sum join(Sum a, Sum b, float c)
     return {m, a.s * exp2_hw((a.m - m) * c) + b.s * exp2_hw((b.m - m) * c)};
 }
 
+// Over groups of W neighbouring lanes; each gets the same.
+template <int W>
+__device__ __forceinline__ Sum join_lanes(Sum a, float c)
+{
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1)
+        a = join(a, Sum{__shfl_xor(a.m, o, kWave), __shfl_xor(a.s, o, kWave)}, c);
+    return a;
+}
+
 // Adds U vectors of logits, the absent ones -inf.
 template <int U, int N>
 __device__ __forceinline__ void add_logits(Sum &a, const fvec<N> (&z)[U], float c)
@@ -66,158 +76,60 @@ __device__ __forceinline__ void add_logits(Sum &a, const fvec<N> (&z)[U], float 
     a = {m, s};
 }
 
-// The sum over columns [c0, c1) of a row, by the whole workgroup; every
-// thread gets it.
-template <typename T, int Threads>
-__device__ __forceinline__ Sum row_sum(const T *z, uint64_t c0, uint64_t c1, float c, Sum *part)
+// Vectors that a lane has in flight.
+constexpr int kFlight = 4;
+
+// Adds columns [c0, c1) of a row, a share of them per thread.  Nt: the row is
+// not read again (2048 x 131072 bf16, loss alone: 80 us, else 85).
+template <typename T, int Threads, bool Nt>
+__device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_t c1, float c)
 {
-    constexpr int N = kVec<T>, U = 4;
+    constexpr int N = kVec<T>, U = kFlight;
     constexpr uint64_t step = (uint64_t)Threads * N;
-    Sum a = {kLowest, 0.0f};
-    fvec<N> f[U];
     uint64_t at = c0 + (uint64_t)threadIdx.x * N;
     for (; at + (U - 1) * step + N <= c1; at += U * step) {
         vec<T, N> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            v[u] = *(const GCQ_G vec<T, N> *)(z + at + u * step);
+            v[u] = dev::ld<Nt>((const GCQ_G vec<T, N> *)(z + at + u * step));
+        fvec<N> f[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             f[u] = to_f32<T, N>(v[u]);
         add_logits<U, N>(a, f, c);
     }
     for (; at < c1; at += step) {
-        fvec<N> g[1];
         const int64_t left = (int64_t)(c1 - at);
-        g[0] = to_f32<T, N>(load_vec<T, N>(z + at, left));
+        fvec<N> f[1] = {to_f32<T, N>(load_vec<T, N>(z + at, left))};
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            g[0][j] = j < left ? g[0][j] : -__builtin_inff();
-        add_logits<1, N>(a, g, c);
-    }
-#pragma unroll
-    for (int o = kWave / 2; o > 0; o >>= 1)
-        a = join(a, Sum{__shfl_xor(a.m, o, kWave), __shfl_xor(a.s, o, kWave)}, c);
-    if ((threadIdx.x & (kWave - 1)) == 0)
-        part[threadIdx.x / kWave] = a;
-    __syncthreads();
-    a = part[0];
-#pragma unroll
-    for (int w = 1; w < Threads / kWave; ++w)
-        a = join(a, part[w], c);
-    return a;
-}
-
-// The sum (or maximum) over the workgroup, in a fixed order; every thread
-// gets it.
-template <int Threads, bool Max>
-__device__ __forceinline__ float block_reduce(float x, float *part)
-{
-    x = Max ? max_lanes(x) : sum_lanes(x);
-    __syncthreads();   // part may still be read
-    if ((threadIdx.x & (kWave - 1)) == 0)
-        part[threadIdx.x / kWave] = x;
-    __syncthreads();
-    x = part[0];
-#pragma unroll
-    for (int w = 1; w < Threads / kWave; ++w)
-        x = Max ? fmaxf(x, part[w]) : x + part[w];
-    return x;
-}
-
-// A row's entries: column (none: 2^32 - 1), probability, and the student's
-// logit there.
-constexpr uint32_t kNone = 0xFFFFFFFFu;
-struct Entries {
-    uint32_t col[GCQ_MAX_TOPK];
-    float p[GCQ_MAX_TOPK], z[GCQ_MAX_TOPK];
-};
-
-template <typename T>
-__device__ __forceinline__ float teacher_logit(const Distill &a, uint64_t row, uint32_t j)
-{
-    if (a.t_f32)
-        return ((const GCQ_G float *)a.top)[row * a.top_ld + j];
-    return (float)((const GCQ_G T *)a.top)[row * a.top_ld + j];
-}
-
-// Fills `e` with the entries in columns [c0, c1); false if the row has none
-// of any weight.  `neg_h` (with Loss): sum of p log p.
-template <typename T, int Threads, bool Loss>
-__device__ __forceinline__ bool load_entries(const Distill &a, uint64_t row, const T *z,
-                                             uint64_t c0, uint64_t c1, Entries &e, float *part,
-                                             float &neg_h)
-{
-    float m = -__builtin_inff();
-    for (uint32_t j = threadIdx.x; j < a.k; j += Threads) {
-        const uint64_t i = row * a.idx_ld + j;
-        const uint64_t col = a.idx64 ? (uint64_t)((const GCQ_G int64_t *)a.idx)[i]
-                                     : (uint64_t)(int64_t)((const GCQ_G int32_t *)a.idx)[i];
-        const bool real = col < a.vocab;
-        const float t = real ? teacher_logit<T>(a, row, j) : -__builtin_inff();
-        e.col[j] = real ? (uint32_t)col : kNone;
-        e.z[j] = col >= c0 && col < c1 ? (float)((const GCQ_G T *)z)[col] : 0.0f;
-        e.p[j] = t;
-        m = fmaxf(m, t);
-    }
-    m = block_reduce<Threads, true>(m, part);
-    if (m == -__builtin_inff())
-        m = 0.0f;   // nothing but absent or -inf entries: the sum is 0 (a NaN shows in it)
-    float s = 0.0f;
-    for (uint32_t j = threadIdx.x; j < a.k; j += Threads)
-        s += expf((e.p[j] - m) / a.temp);
-    s = block_reduce<Threads, false>(s, part);
-    const float ls = logf(s);
-    float h = 0.0f;
-    for (uint32_t j = threadIdx.x; j < a.k; j += Threads) {
-        const float l = (e.p[j] - m) / a.temp, p = expf(l) / s;
-        e.p[j] = p;
-        if (p != 0.0f)
-            h += p * (l - ls);
-    }
-    if constexpr (Loss)
-        neg_h = block_reduce<Threads, false>(h, part);
-    __syncthreads();   // e is whole
-    return s != 0.0f;
-}
-
-// dz at the entries' columns in [c0, c1), over what the dense pass wrote
-// there (after a barrier).  A column named twice loses both probabilities;
-// each of its entries writes the same sum.
-template <typename T, int Threads, typename Q>
-__device__ __forceinline__ void put_entries(const Distill &a, const Entries &e, T *dz, uint64_t c0,
-                                            uint64_t c1, float g, Q q)
-{
-    for (uint32_t j = threadIdx.x; j < a.k; j += Threads) {
-        const uint32_t col = e.col[j];
-        if (col == kNone || col < c0 || col >= c1)
-            continue;
-        float p = 0.0f;
-        for (uint32_t i = 0; i < a.k; ++i)
-            p += e.col[i] == col ? e.p[i] : 0.0f;
-        ((GCQ_G T *)dz)[col] = (T)(g * (q(e.z[j]) - p));
+            f[0][j] = j < left ? f[0][j] : -__builtin_inff();
+        add_logits<1, N>(a, f, c);
     }
 }
 
-// dz = value(z) over columns [c0, c1).
+// dz = value(z) over columns [c0, c1).  Non-temporal on both sides: the
+// logits are read for the last time and dz is not read here, so the rows
+// still to be read keep the caches (2048 x 131072 bf16 from a kept lse: 175
+// us, with ordinary loads 195).
 template <typename T, int Threads, typename F>
 __device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t c1, F value)
 {
-    constexpr int N = kVec<T>, U = 4;
+    constexpr int N = kVec<T>, U = kFlight;
     constexpr uint64_t step = (uint64_t)Threads * N;
     uint64_t at = c0 + (uint64_t)threadIdx.x * N;
     for (; at + (U - 1) * step + N <= c1; at += U * step) {
         vec<T, N> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            v[u] = *(const GCQ_G vec<T, N> *)(z + at + u * step);
+            v[u] = dev::ld<true>((const GCQ_G vec<T, N> *)(z + at + u * step));
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             fvec<N> f = to_f32<T, N>(v[u]);
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 f[j] = value(f[j]);
-            *(GCQ_G vec<T, N> *)(dz + at + u * step) = from_f32<T, N>(f);
+            dev::st<true>((GCQ_G vec<T, N> *)(dz + at + u * step), from_f32<T, N>(f));
         }
     }
     for (; at < c1; at += step) {
@@ -226,7 +138,7 @@ __device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t
 #pragma unroll
         for (int j = 0; j < N; ++j)
             f[j] = value(f[j]);
-        store_vec<T, N>(dz + at, from_f32<T, N>(f), left);
+        store_vec<T, N, true>(dz + at, from_f32<T, N>(f), left);
     }
 }
 
@@ -236,17 +148,151 @@ __device__ __forceinline__ void zero_row(T *dz, uint64_t c0, uint64_t c1)
     constexpr int N = kVec<T>;
     const vec<T, N> zero = (T)0.0f;
     for (uint64_t at = c0 + (uint64_t)threadIdx.x * N; at < c1; at += (uint64_t)Threads * N)
-        store_vec<T, N>(dz + at, zero, (int64_t)(c1 - at));
+        store_vec<T, N, true>(dz + at, zero, (int64_t)(c1 - at));
 }
 
-// Loss and lse, and with Grad dz too: a workgroup per row.  The second pass
-// finds the row in the caches.
+constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+template <typename T>
+__device__ __forceinline__ float teacher_logit(const Distill &a, uint64_t row, uint32_t j)
+{
+    if (a.t_f32)
+        return ((const GCQ_G float *)a.top)[row * a.top_ld + j];
+    return (float)((const GCQ_G T *)a.top)[row * a.top_ld + j];
+}
+
+// A teacher's entry: column (kNone: absent), logit (absent: -inf), the
+// student's logit there.
+struct Entry {
+    uint32_t col;
+    float top, at;
+};
+
+template <typename T>
+__device__ __forceinline__ Entry load_entry(const Distill &a, uint64_t row, uint32_t j)
+{
+    Entry e = {kNone, -__builtin_inff(), 0.0f};
+    if (j < a.k) {
+        const uint64_t i = row * a.idx_ld + j;
+        const uint64_t col = a.idx64 ? (uint64_t)((const GCQ_G int64_t *)a.idx)[i]
+                                     : (uint64_t)(int64_t)((const GCQ_G int32_t *)a.idx)[i];
+        const float t = teacher_logit<T>(a, row, j);
+        if (col < a.vocab) {
+            e.col = (uint32_t)col;
+            e.top = t;
+        }
+    }
+    return e;
+}
+
+// A row's entries: the thread's first in a register (loaded before the row is
+// read), those beyond the workgroup's threads in LDS.  Dynamic LDS: k columns,
+// k weights and k student's logits.
+template <typename T, int Threads>
+struct Entries {
+    static constexpr int Waves = Threads / kWave;
+    uint32_t *col;
+    float *w, *z;
+    Entry own;
+
+    __device__ __forceinline__ Entries(void *lds, uint32_t k)
+        : col((uint32_t *)lds), w((float *)lds + k), z((float *)lds + 2 * k)
+    {
+    }
+
+    // The student's logits at the entries whose column is in [c0, c1).
+    __device__ __forceinline__ void read_logits(const Distill &a, uint64_t row, const T *zr,
+                                                uint64_t c0, uint64_t c1)
+    {
+        const GCQ_G T *p = (const GCQ_G T *)zr;
+        if (own.col != kNone && own.col >= c0 && own.col < c1)
+            own.at = (float)p[own.col];
+        for (uint32_t j = threadIdx.x + Threads; j < a.k; j += Threads) {
+            const Entry e = load_entry<T>(a, row, j);
+            col[j] = e.col;
+            w[j] = e.top;
+            z[j] = e.col != kNone && e.col >= c0 && e.col < c1 ? (float)p[e.col] : 0.0f;
+        }
+    }
+
+    // The thread's largest teacher logit.
+    __device__ __forceinline__ float top(const Distill &a) const
+    {
+        float m = own.top;
+        for (uint32_t j = threadIdx.x + Threads; j < a.k; j += Threads)
+            m = fmaxf(m, w[j]);
+        return m;
+    }
+
+    // Turns teacher logits into weights exp((t - m) / T) and adds up the
+    // thread's: of w, of w log w and of w (z - zm) / T.
+    __device__ __forceinline__ void weigh(const Distill &a, float m, float zm, float (&sum)[3])
+    {
+        auto one = [&](uint32_t j, float t, float at) {
+            const float l = (t - m) / a.temp, e = expf(l);
+            if (e != 0.0f) {
+                sum[0] += e;
+                sum[1] += e * l;
+                sum[2] += e * ((at - zm) / a.temp);
+            }
+            w[j] = e;
+        };
+        if (threadIdx.x < a.k) {
+            col[threadIdx.x] = own.col;
+            one(threadIdx.x, own.top, own.at);
+        }
+        for (uint32_t j = threadIdx.x + Threads; j < a.k; j += Threads)
+            one(j, w[j], z[j]);
+    }
+
+    // dz at the entries' columns in [c0, c1), over what was stored there
+    // before a barrier.  A column named twice loses both probabilities: each
+    // of its entries writes the same sum.
+    template <typename Q>
+    __device__ __forceinline__ void put(const Distill &a, T *dz, uint64_t c0, uint64_t c1, float g,
+                                        float sw, Q q) const
+    {
+        for (uint32_t j = threadIdx.x; j < a.k; j += Threads) {
+            const uint32_t cj = col[j];
+            if (cj == kNone || cj < c0 || cj >= c1)
+                continue;
+            float p = 0.0f;
+#pragma unroll 4
+            for (uint32_t i = 0; i < a.k; ++i)
+                p += col[i] == cj ? w[i] : 0.0f;
+            ((GCQ_G T *)dz)[cj] = (T)(g * (q(j == threadIdx.x ? own.at : z[j]) - p / sw));
+        }
+    }
+};
+
+// A value per thread -> the workgroup's sum (or maximum), the same for every
+// thread; `part` is used by one reduction between two barriers.
+template <int Waves, bool Max>
+__device__ __forceinline__ void reduce_put(float x, float *part)
+{
+    x = Max ? max_lanes(x) : sum_lanes(x);
+    if ((threadIdx.x & (kWave - 1)) == 0)
+        part[threadIdx.x / kWave] = x;
+}
+
+template <int Waves, bool Max>
+__device__ __forceinline__ float reduce_get(const float *part)
+{
+    const float x = part[threadIdx.x % Waves];
+    return Max ? max_lanes<Waves>(x) : sum_lanes<Waves>(x);
+}
+
+// Loss and lse, and with Grad dz too: a workgroup per row.  The entries'
+// loads travel while the row is summed; the second pass finds what it reads
+// again in the caches.
 template <typename T, int Threads, bool Grad>
 __global__ __launch_bounds__(Threads) void distill_loss_kernel(Distill a)
 {
-    __shared__ Entries e;
-    __shared__ float part[Threads / kWave];
-    __shared__ Sum sums[Threads / kWave];
+    constexpr int N = kVec<T>, Waves = Threads / kWave;
+    extern __shared__ __align__(16) uint32_t lds[];
+    __shared__ Sum sum_s[Waves];
+    __shared__ float top_s[Waves], red_s[3][Waves];
+    const uint32_t tid = threadIdx.x;
     const uint64_t row = block_number();
     if (row >= a.rows)
         return;
@@ -254,7 +300,7 @@ __global__ __launch_bounds__(Threads) void distill_loss_kernel(Distill a)
     T *dz = (T *)a.dz + row * a.dz_ld;
     const float s = a.row_scale ? a.scale * a.row_scale[row] : a.scale;
     if (s == 0.0f) {
-        if (threadIdx.x == 0) {
+        if (tid == 0) {
             a.loss[row] = 0.0f;
             a.lse_out[row] = 0.0f;
         }
@@ -262,19 +308,38 @@ __global__ __launch_bounds__(Threads) void distill_loss_kernel(Distill a)
             zero_row<T, Threads>(dz, 0, a.vocab);
         return;
     }
-    float neg_h;
-    const bool any = load_entries<T, Threads, true>(a, row, z, 0, a.vocab, e, part, neg_h);
+    Entries<T, Threads> e(lds, a.k);
+    e.own = load_entry<T>(a, row, tid);
     const float c = kLog2e / a.temp;
-    const Sum r = row_sum<T, Threads>(z, 0, a.vocab, c, sums);
-    const float lz = logf(r.s);
-    float x = 0.0f;   // cross entropy with q
-    for (uint32_t j = threadIdx.x; j < a.k; j += Threads)
-        if (e.p[j] != 0.0f)
-            x += e.p[j] * ((e.z[j] - r.m) / a.temp - lz);
-    x = block_reduce<Threads, false>(x, part);
-    if (threadIdx.x == 0) {
+    Sum r = {kLowest, 0.0f};
+    const uint64_t half = a.vocab / (2 * Threads * N) * (Threads * N);
+    add_row<T, Threads, !Grad>(r, z, 0, half, c);
+    e.read_logits(a, row, z, 0, a.vocab);
+    add_row<T, Threads, !Grad>(r, z, half, a.vocab, c);
+    r = join_lanes<kWave>(r, c);
+    if ((tid & (kWave - 1)) == 0)
+        sum_s[tid / kWave] = r;
+    reduce_put<Waves, true>(e.top(a), top_s);
+    __syncthreads();
+    r = join_lanes<Waves>(sum_s[tid % Waves], c);
+    float tm = reduce_get<Waves, true>(top_s);
+    if (tm == -__builtin_inff())
+        tm = 0.0f;   // nothing but absent or -inf entries: their sum is 0 (a NaN shows in it)
+    float w[3] = {0.0f, 0.0f, 0.0f};
+    e.weigh(a, tm, r.m, w);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        reduce_put<Waves, false>(w[i], red_s[i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        w[i] = reduce_get<Waves, false>(red_s[i]);
+    const bool any = w[0] != 0.0f;
+    if (tid == 0) {
+        const float lz = logf(r.s);
         // no finite logit: nothing of q is left where p is
-        const float kl = r.s == 0.0f ? __builtin_inff() : neg_h - x;
+        const float kl = r.s == 0.0f ? __builtin_inff()
+                                     : w[1] / w[0] - logf(w[0]) - (w[2] / w[0] - lz);
         a.loss[row] = any ? s * kl : 0.0f;
         a.lse_out[row] = r.m / a.temp + lz;
     }
@@ -283,23 +348,26 @@ __global__ __launch_bounds__(Threads) void distill_loss_kernel(Distill a)
             zero_row<T, Threads>(dz, 0, a.vocab);
             return;
         }
-        const float g = s / a.temp, f = g / r.s, inv = 1.0f / r.s;
+        const float g = s / a.temp, inv = 1.0f / r.s, f = g / r.s;
         map_row<T, Threads>(z, dz, 0, a.vocab,
-                            [=](float v) { return exp2_hw((v - r.m) * c) * f; });
+                               [=](float x) { return exp2_hw((x - r.m) * c) * f; });
         __syncthreads();
-        put_entries<T, Threads>(a, e, dz, 0, a.vocab, g,
-                                [=](float v) { return exp2_hw((v - r.m) * c) * inv; });
+        e.put(a, dz, 0, a.vocab, g, w[0],
+              [=](float x) { return exp2_hw((x - r.m) * c) * inv; });
     }
 }
 
-// dz from a kept lse; `parts` workgroups share a row, `chunk` columns each.  The exponent is
-// ((z - hi) - lo) log2(e) / T with hi + lo = lse T: exact where q is large.
+// dz from a kept lse; `parts` workgroups share a row, `chunk` columns each.
+// The exponent is ((z - hi) - lo) log2(e) / T with hi + lo = lse T: exact
+// where q is large.  Whether the row has entries at all is known only after
+// the dense pass; a row without is zeroed then.
 template <typename T, int Threads>
 __global__ __launch_bounds__(Threads) void distill_grad_kernel(Distill a, uint64_t parts,
                                                                uint64_t chunk)
 {
-    __shared__ Entries e;
-    __shared__ float part[Threads / kWave];
+    constexpr int Waves = Threads / kWave;
+    extern __shared__ __align__(16) uint32_t lds[];
+    __shared__ float top_s[Waves], red_s[Waves];
     const uint64_t row = block_number() / parts, c0 = block_number() % parts * chunk;
     if (row >= a.rows)
         return;
@@ -312,27 +380,55 @@ __global__ __launch_bounds__(Threads) void distill_grad_kernel(Distill a, uint64
         zero_row<T, Threads>(dz, c0, c1);
         return;
     }
-    float unused;
-    if (!load_entries<T, Threads, false>(a, row, z, c0, c1, e, part, unused)) {
-        zero_row<T, Threads>(dz, c0, c1);
-        return;
-    }
+    Entries<T, Threads> e(lds, a.k);
+    e.own = load_entry<T>(a, row, threadIdx.x);
+    e.read_logits(a, row, z, c0, c1);
+    if (a.dz == a.z)
+        __syncthreads();   // in place: they are read before any is written
     const float c = kLog2e / a.temp, g = s / a.temp;
     const float hi = lse * a.temp, lo = fmaf(lse, a.temp, -hi);
-    const auto q = [=](float v) { return exp2_hw(((v - hi) - lo) * c); };
-    map_row<T, Threads>(z, dz, c0, c1, [=](float v) { return q(v) * g; });
+    const auto q = [=](float x) { return exp2_hw(((x - hi) - lo) * c); };
+    map_row<T, Threads>(z, dz, c0, c1, [=](float x) { return q(x) * g; });
+    reduce_put<Waves, true>(e.top(a), top_s);
     __syncthreads();
-    put_entries<T, Threads>(a, e, dz, c0, c1, g, q);
+    float tm = reduce_get<Waves, true>(top_s);
+    if (tm == -__builtin_inff())
+        tm = 0.0f;
+    float w[3] = {0.0f, 0.0f, 0.0f};
+    e.weigh(a, tm, 0.0f, w);
+    reduce_put<Waves, false>(w[0], red_s);
+    __syncthreads();
+    const float sw = reduce_get<Waves, false>(red_s);
+    if (sw == 0.0f)
+        zero_row<T, Threads>(dz, c0, c1);
+    else
+        e.put(a, dz, c0, c1, g, sw, q);
+}
+
+template <typename T, int Threads>
+void loss(const Distill &a, hipStream_t s)
+{
+    if (a.dz)
+        distill_loss_kernel<T, Threads, true><<<block_grid(a.rows), Threads, 12 * a.k, s>>>(a);
+    else
+        distill_loss_kernel<T, Threads, false><<<block_grid(a.rows), Threads, 12 * a.k, s>>>(a);
 }
 
 template <typename T>
 hipError_t loss(const Distill &a, hipStream_t s)
 {
-    const dim3 rows = block_grid(a.rows);
-    if (a.dz)
-        distill_loss_kernel<T, 512, true><<<rows, 512, 0, s>>>(a);
+    // threads for one pass of a few vectors each, U in flight; rows of 8192 x
+    // 131072 bytes and more in flight at once no longer stay in the caches
+    // between the two passes, so long rows get few, large workgroups
+    const uint64_t bytes = a.vocab * sizeof(T);
+    if (bytes <= 8192)
+        loss<T, 64>(a, s);
+    else if (bytes <= 32768)
+        loss<T, 256>(a, s);
+    else if (bytes <= 98304)
+        loss<T, 512>(a, s);
     else
-        distill_loss_kernel<T, 512, false><<<rows, 512, 0, s>>>(a);
+        loss<T, 1024>(a, s);
     return hipGetLastError();
 }
 
@@ -340,10 +436,10 @@ template <typename T>
 hipError_t grad(const Distill &a, hipStream_t s)
 {
     constexpr int threads = 256;
-    const uint64_t chunk = (uint64_t)threads * kVec<T> * 16;
+    const uint64_t chunk = (uint64_t)threads * kVec<T> * 8;
     const uint64_t parts = (a.vocab + chunk - 1) / chunk;
     distill_grad_kernel<T, threads>
-        <<<block_grid(a.rows * parts), threads, 0, s>>>(a, parts, chunk);
+        <<<block_grid(a.rows * parts), threads, 12 * a.k, s>>>(a, parts, chunk);
     return hipGetLastError();
 }
 

@@ -107,7 +107,6 @@ def test_against_plain(gpu, kind, index, T):
         assert (wide[:, V:] == 7.0).all()
         both = gpu.distill_loss_grad(z, idx, top.float() if n % 2 else top, T, row_scale, scale)
         check(both, want, V, kind)
-        assert torch.equal(both[0], loss) and torch.equal(both[1], lse)
         z2 = z.clone()
         assert torch.equal(gpu.distill_loss_grad(z2, idx, top, T, row_scale, scale, out=z2)[2], both[2])
         z2 = z.clone()
