@@ -130,6 +130,8 @@ constexpr uint32_t kSortThreads = 512, kSortItems = 4;
 constexpr uint32_t kSortTile = kSortThreads * kSortItems;
 // Up to this many tiles each scatter sums the tiles' counts itself; beyond, a
 // launch of its own scans them (a scatter's own reading grows with the square).
+// Counting every key in each scatter, to save the launch that counts, took
+// longer from 10000 positions on: the frequent tokens' LDS atomics collide.
 constexpr uint32_t kSumTiles = 128;
 
 __device__ __forceinline__ void wave_order()
@@ -368,12 +370,13 @@ __global__ __launch_bounds__(256) void embed_starts_kernel(const uint32_t *__res
 }
 
 // Both at once by one workgroup: the starts counted from the first position,
-// the tiles' counts 0 but for the total.
+// the tiles' counts 0.
 __global__ __launch_bounds__(1024) void embed_starts_small_kernel(const uint32_t *__restrict__ keys,
                                                                   uint32_t n, uint32_t vocab,
                                                                   uint32_t run,
                                                                   uint32_t *__restrict__ starts,
-                                                                  uint32_t *__restrict__ tiles)
+                                                                  uint32_t *__restrict__ tiles,
+                                                                  int32_t *__restrict__ count)
 {
     __shared__ uint32_t sums[1024 / kWave];
     constexpr uint32_t per = kSmallStarts / 1024u;
@@ -389,15 +392,17 @@ __global__ __launch_bounds__(1024) void embed_starts_small_kernel(const uint32_t
     const uint32_t before = block_scan<1024>(mine, sums, total);
     if (i0 < n && i0 % run == 0)
         starts[i0 / run] = before;
-    const uint32_t count = (n + kEmbedTile - 1) / kEmbedTile;
-    if (threadIdx.x <= count)
-        tiles[threadIdx.x] = threadIdx.x < count ? 0u : total;
+    if (threadIdx.x < (n + kEmbedTile - 1) / kEmbedTile)
+        tiles[threadIdx.x] = 0u;
+    if (threadIdx.x == 0)
+        *count = (int32_t)total;
 }
 
-// In-place exclusive scan of a[0..m) by one workgroup, the total to a[m].
+// In-place exclusive scan of a[0..m) by one workgroup, the total to a[m] (and
+// *count).
 constexpr uint32_t kScanThreads = 1024, kScanItems = 8;
 __global__ __launch_bounds__(kScanThreads) void embed_scan_kernel(uint32_t *__restrict__ a,
-                                                                  uint64_t m)
+                                                                  uint64_t m, int32_t *count)
 {
     __shared__ uint32_t sums[kScanThreads / kWave];
     uint32_t carry = 0;
@@ -418,11 +423,32 @@ __global__ __launch_bounds__(kScanThreads) void embed_scan_kernel(uint32_t *__re
         }
         carry += total;
     }
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         a[m] = carry;
+        if (count)
+            *count = (int32_t)carry;
+    }
 }
 
 enum class Form { kWrite, kAdd, kRows };
+
+__device__ __forceinline__ uint32_t sum_counts(uint32_t x)
+{
+#pragma unroll
+    for (int o = kWave / 2; o > 0; o >>= 1)
+        x += (uint32_t)__shfl_xor((int)x, o, kWave);
+    return x;
+}
+
+// Segment starts before a tile: scanned, or the sum of up to 64 tiles' counts
+// by the wavefront.
+__device__ __forceinline__ uint32_t starts_before(const EmbedGrad &e, uint64_t tile)
+{
+    if (e.scanned)
+        return e.tiles[tile];
+    const uint32_t lane = threadIdx.x & (kWave - 1);
+    return sum_counts(lane < tile ? e.tiles[lane] : 0u);
+}
 
 // p[0..count) = 0 by 256 threads, in aligned vectors but for the ends.
 __device__ __forceinline__ void zero_floats(float *p, uint64_t count)
@@ -521,15 +547,19 @@ __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64
     store_vec<float, N, true>(e.out + row * e.out_ld + c, v, left);
 }
 
-// One pass over g in sorted order.  L lanes (a power of two up to 256) share
-// a run of e.run sorted positions and L * N columns.  A segment inside the
-// run is finished here; one that reaches over an end leaves its sum in
-// part[run][0] (it began before the run) or part[run][1].  kWrite: the
-// workgroups behind the first `blocks` zero the rows that no position names.
+// One pass over g in sorted order.  A wavefront takes a run of e.run sorted
+// positions and 256 columns (4 a lane: 16-byte stores; with 8 a lane the sums
+// of 16-bit rows went out as pairs of stores 32 bytes apart and took a fifth
+// longer).  Keys and positions are the wavefront's own, so they are scalar
+// loads and every branch on them is uniform.  A segment inside the run is
+// finished here; one that reaches over an end leaves its sum in part[run][0]
+// (it began before the run) or part[run][1].  kWrite: the workgroups behind
+// the first `blocks` zero the rows that no position names.
 template <typename T, Form F>
-__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t lanes, uint32_t cols,
+__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t cols,
                                                          uint64_t blocks, uint32_t span)
 {
+    using Scalar = const __attribute__((address_space(4))) uint32_t;
     constexpr int N = 4, U = F == Form::kAdd ? 4 : 8;
     const uint64_t block = block_number();
     if constexpr (F == Form::kWrite) {
@@ -540,116 +570,118 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t l
             return;
         }
     }
-    __shared__ uint32_t key_s[32 * (kEmbedRun + 2)], pos_s[32 * kEmbedRun];
-    const uint32_t groups = 256u / lanes, lane = threadIdx.x & (lanes - 1);
-    const uint32_t slot = threadIdx.x / lanes, R = e.run;
-    const uint64_t run0 = block / cols * groups;
-    const uint64_t n = e.n;
-    // key_s[s][1 + i]: the run's keys, with one neighbour on each side
-    // (beyond the ends: no key at all, 2^32 - 1)
-    for (uint32_t i = threadIdx.x; i < groups * (R + 2); i += 256u) {
-        const uint32_t s = i / (R + 2), j = i % (R + 2);
-        const uint64_t at = (run0 + s) * R + j;   // one past the position
-        key_s[i] = at >= 1 && at <= n ? e.keys[at - 1] : 0xFFFFFFFFu;
-        if (j < R)
-            pos_s[s * R + j] = at < n ? e.order[at] : 0u;
-    }
-    __syncthreads();
-    const uint64_t run = run0 + slot, i0 = run * R;
-    const uint64_t c = (block % cols * lanes + lane) * N;
-    if (i0 >= n || c >= e.dim)
+    const uint32_t lane = threadIdx.x & (kWave - 1);
+    const uint64_t item =
+        block * 4u + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    const uint64_t run = item / cols, n = e.n, i0 = run * e.run;
+    const uint64_t c = (item % cols * kWave + lane) * N;
+    if (i0 >= n)
         return;
-    const uint32_t len = n - i0 < R ? (uint32_t)(n - i0) : R;
-    const uint32_t *key = key_s + slot * (R + 2) + 1, *pos = pos_s + slot * R;
-    const int64_t left = (int64_t)(e.dim - c);
+    Scalar *keys = (Scalar *)e.keys, *order = (Scalar *)e.order;
+    const uint64_t end = n - i0 < e.run ? n : i0 + e.run;
+    const int64_t left = c < e.dim ? (int64_t)(e.dim - c) : 0;
     const T *g = (const T *)e.g + c;
     uint64_t seat = 0;
     if constexpr (F == Form::kRows)
-        seat = (uint64_t)e.tiles[i0 / kEmbedTile] + e.starts[run] - 1u;   // of the segment open here
-    const bool heads = key[0] == key[-1];   // the first segment began before the run
+        seat = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(
+                   (int)starts_before(e, i0 / kEmbedTile)) +
+               ((Scalar *)e.starts)[run] - 1u;   // of the segment open here
+    if constexpr (F == Form::kRows) {
+        if (item == 0 && !e.scanned) {
+            const uint32_t all = starts_before(e, (n + kEmbedTile - 1) / kEmbedTile);
+            if (lane == 0)
+                *e.count = (int32_t)all;
+        }
+    }
+    uint32_t last = i0 ? keys[i0 - 1] : 0xFFFFFFFFu;   // the key before
+    bool head = last == keys[i0];   // the open segment began before the run
     fvec<N> acc = 0.0f;
-    for (uint32_t b = 0; b < len; b += U) {
+    for (uint64_t b = i0; b < end; b += U) {
+        uint32_t key[U + 1], pos[U];   // beyond the end: no key at all, 2^32 - 1
+#pragma unroll
+        for (int j = 0; j <= U; ++j)
+            key[j] = b + j < n ? keys[b + j] : 0xFFFFFFFFu;
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            pos[j] = b + j < n ? order[b + j] : 0u;
         vec<T, N> v[U];
         fvec<N> old[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const uint32_t i = b + j;
             v[j] = (T)0.0f;
             old[j] = 0.0f;
-            if (i < len && key[i] < e.vocab) {
-                if (pos[i] < n)
-                    v[j] = load_vec<T, N, true>(g + pos[i] * e.ld, left);
+            if (key[j] < e.vocab && pos[j] < n) {   // padding is not read
+                if (left > 0)
+                    v[j] = load_vec<T, N, true>(g + pos[j] * e.ld, left);
                 if constexpr (F == Form::kAdd)
-                    if (key[i] != key[i + 1])
-                        old[j] = load_vec<float, N, true>(e.out + key[i] * e.out_ld + c, left);
+                    if (key[j] != key[j + 1] && left > 0)
+                        old[j] = load_vec<float, N, true>(e.out + key[j] * e.out_ld + c, left);
             }
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const uint32_t i = b + j;
-            if (i >= len)
-                break;
-            const uint32_t k = key[i];
+            const uint32_t k = key[j];
             if (k >= e.vocab)
-                break;   // padding: so is everything behind it
-            const bool opens = k != key[(int)i - 1];
-            if constexpr (F == Form::kRows) {
-                if (opens) {
+                return;   // padding, or the end: so is everything behind it
+            const fvec<N> f = to_f32<T, N>(v[j]);
+            if (k != last) {
+                acc = f;
+                head = false;
+                if constexpr (F == Form::kRows) {
                     ++seat;
                     if (c == 0)
                         e.ids[seat] = (int32_t)k;
                 }
-            }
-            const fvec<N> f = to_f32<T, N>(v[j]);
-            acc = opens || i == 0 ? f : acc + f;
-            const bool closes = k != key[i + 1];
-            if (!closes && i + 1 < len)
-                continue;
-            const bool head = heads && key[0] == k;
-            if (closes && !head) {
-                put_row<F, N>(e, F == Form::kRows ? seat : k, c, acc, old[j], left);
             } else {
-                float *p = e.part + (2 * run + (head ? 0 : 1)) * e.dim + c;
-                store_vec<float, N>(p, acc, left);
+                acc += f;
+            }
+            last = k;
+            if (k != key[j + 1]) {
+                if (left > 0) {
+                    if (head)
+                        store_vec<float, N>(e.part + 2 * run * e.dim + c, acc, left);
+                    else
+                        put_row<F, N>(e, F == Form::kRows ? seat : k, c, acc, old[j], left);
+                }
+            } else if (b + j + 1 == end && left > 0) {
+                store_vec<float, N>(e.part + (2 * run + (head ? 0 : 1)) * e.dim + c, acc, left);
             }
         }
-    }
-    if constexpr (F == Form::kRows) {
-        if (i0 == 0 && c == 0)
-            *e.count = (int32_t)e.tiles[(n + kEmbedTile - 1) / kEmbedTile];
     }
 }
 
 // Joins the segments that reach over the end of the run they begin in: part
-// 1 of that run, then part 0 of the following ones.  A workgroup looks at 16
-// runs and 256 columns; a wavefront adds up a segment of at most kJoinShort
-// parts by itself, longer ones are shared by all 8 (consecutive parts each,
-// their sums added in order).
-constexpr uint32_t kJoinThreads = 512, kJoinRuns = 8, kJoinShort = 16, kJoinBatch = 8;
+// 1 of that run, then part 0 of the following ones.  A workgroup looks at 8
+// runs and 256 columns.  A segment of at most kJoinShort parts is one
+// wavefront's, four columns a lane; a longer one is shared by all 8: 32
+// columns each, 8 groups of lanes taking consecutive shares of the parts, whose
+// sums are added in a fixed order.  No LDS and no barrier: with the shares
+// joined through LDS the short segments slowed down too (16384 positions into
+// 131072 x 4096: 115 us against 105).
+constexpr uint32_t kJoinThreads = 512, kJoinRuns = 8, kJoinShort = 8, kJoinBatch = 4;
 template <Form F>
-__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, uint64_t runs)
+__global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e)
 {
     constexpr int N = 4;
     constexpr uint32_t waves = kJoinThreads / kWave;
-    __shared__ fvec<N> share[waves][kWave];
     const uint32_t lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, R = e.run;
-    const uint64_t c = ((uint64_t)blockIdx.y * kWave + lane) * N;
-    const int64_t left = c < e.dim ? (int64_t)(e.dim - c) : 0;
-    const uint64_t run0 = (uint64_t)blockIdx.x * kJoinRuns;
-    // every wavefront: lane l holds the last key of run run0 + l and the first
-    // key of the one behind it, and whether the run begins a segment that
-    // reaches over its end
+    const uint64_t run0 = (uint64_t)blockIdx.x * kJoinRuns, col0 = (uint64_t)blockIdx.y * 256u;
+    // every wavefront: lane l holds the last key of run run0 + l (of this
+    // window's runs) and the first key of the one behind it, and whether the
+    // run begins a segment that reaches over its end
     uint32_t k0 = 0xFFFFFFFFu, next = 0xFFFFFFFFu, prev = 0xFFFFFFFFu;
     {
         const uint64_t i0 = (run0 + lane) * R, end = i0 + R;
         if (end < e.n) {
-            k0 = e.keys[end - 1];
             next = e.keys[end];
-            if (i0)
-                prev = e.keys[i0 - 1];
+            if (lane < kJoinRuns) {
+                k0 = e.keys[end - 1];
+                if (i0)
+                    prev = e.keys[i0 - 1];
+            }
         }
     }
-    const bool joins = lane < kJoinRuns && k0 < e.vocab && next == k0 && prev != k0;
+    const bool joins = k0 < e.vocab && next == k0 && prev != k0;
     uint32_t turn = 0;
     for (uint64_t m = __ballot(joins); m; m &= m - 1, ++turn) {
         const uint32_t q = (uint32_t)__builtin_ctzll(m);
@@ -670,50 +702,57 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e, u
         const bool alone = parts <= kJoinShort;
         if (alone && turn % waves != wave)
             continue;
+        const uint64_t c = col0 + (alone ? lane * N : wave * 32u + lane % 8u * N);
+        const int64_t left = c < e.dim ? (int64_t)(e.dim - c) : 0;
+        const uint64_t each = alone ? parts : (parts + 7u) / 8u;
+        const uint64_t p0 = alone ? 0 : lane / 8u * each;
+        const uint64_t p1 = p0 + each < parts ? p0 + each : parts;
+        // what the row's place takes is loaded ahead of the parts
         fvec<N> old = 0.0f;
-        if constexpr (F == Form::kAdd)
+        uint32_t before = 0, starts = 0, mine = 0, ahead = 0;
+        if constexpr (F == Form::kAdd) {
             if (left > 0)
                 old = load_vec<float, N>(e.out + (uint64_t)k * e.out_ld + c, left);
-        const uint64_t each = alone ? parts : (parts + waves - 1) / waves;
-        const uint64_t p0 = alone ? 0 : wave * each, p1 = p0 + each < parts ? p0 + each : parts;
+        } else if constexpr (F == Form::kRows) {
+            const uint64_t tile = run * R / kEmbedTile;
+            before = e.scanned ? e.tiles[tile] : lane < tile ? e.tiles[lane] : 0u;
+            starts = e.starts[run];
+            const uint64_t i = run * R + lane;
+            if (lane < R) {
+                mine = e.keys[i];
+                ahead = i ? e.keys[i - 1] : 0xFFFFFFFFu;
+            }
+        }
         fvec<N> acc = 0.0f;
-        for (uint64_t p = p0; p < p1; p += kJoinBatch) {
+        for (uint64_t b = 0; b < each; b += kJoinBatch) {
             vec<float, N> v[kJoinBatch];
 #pragma unroll
             for (uint32_t u = 0; u < kJoinBatch; ++u) {
+                const uint64_t p = p0 + b + u;
                 v[u] = 0.0f;
-                if (p + u < p1 && left > 0)
-                    v[u] = load_vec<float, N>(
-                        e.part + (2 * (run + p + u) + (p + u ? 0 : 1)) * e.dim + c, left);
+                if (p < p1 && b + u < each && left > 0)
+                    v[u] = load_vec<float, N>(e.part + (2 * (run + p) + (p ? 0 : 1)) * e.dim + c,
+                                              left);
             }
 #pragma unroll
             for (uint32_t u = 0; u < kJoinBatch; ++u)
                 acc += v[u];
         }
+        if (!alone) {
+#pragma unroll
+            for (int o = 8; o < kWave; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    acc[i] += __shfl_xor(acc[i], o, kWave);
+        }
         uint64_t row = k;
         if constexpr (F == Form::kRows) {
             // the last segment that opens in this run
-            bool opens = false;
-            if (lane < R) {
-                const uint64_t i = run * R + lane;
-                opens = i == 0 || e.keys[i] != e.keys[i - 1];
-            }
-            row = (uint64_t)e.tiles[run * R / kEmbedTile] + e.starts[run] +
-                  (uint32_t)__popcll(__ballot(opens)) - 1u;
+            const uint32_t opens = (uint32_t)__popcll(__ballot(mine != ahead));
+            row = (uint64_t)(e.scanned ? before : sum_counts(before)) + starts + opens - 1u;
         }
-        if (alone) {
-            if (left > 0)
-                put_row<F, N>(e, row, c, acc, old, left);
-            continue;
-        }
-        __syncthreads();   // share may still be read
-        share[wave][lane] = acc;
-        __syncthreads();
-        if (wave == 0 && left > 0) {
-            for (uint32_t w = 1; w < waves && w * each < parts; ++w)
-                acc += share[w][lane];
+        if (left > 0 && (alone || lane < 8u))
             put_row<F, N>(e, row, c, acc, old, left);
-        }
     }
 }
 
@@ -826,29 +865,31 @@ hipError_t sort_tokens(const I *tokens, uint32_t n, uint64_t vocab, uint32_t *pl
 template <typename T, Form F>
 void sum_runs(const EmbedGrad &e, uint64_t runs, hipStream_t s)
 {
-    const uint32_t lanes = lanes_for(e.dim, 4), groups = 256u / lanes;
-    const uint32_t cols = (uint32_t)((e.dim + 4ull * lanes - 1) / (4ull * lanes));
-    const uint64_t blocks = (runs + groups - 1) / groups * cols;
+    const uint32_t cols = (uint32_t)((e.dim + 255) / 256);
+    const uint64_t blocks = (runs * cols + 3) / 4;
     // rows that a zeroing workgroup looks at: about 64 KiB, 64 at most
     const uint32_t span = (uint32_t)(e.dim >= 16384 ? 1u : e.dim <= 256 ? 64u : 16384 / e.dim);
     const uint64_t zero = F == Form::kWrite ? (e.vocab + span - 1) / span : 0;
-    embed_grad_kernel<T, F><<<block_grid(blocks + zero), 256, 0, s>>>(e, lanes, cols, blocks, span);
+    embed_grad_kernel<T, F><<<block_grid(blocks + zero), 256, 0, s>>>(e, cols, blocks, span);
 }
 
 template <Form F>
-hipError_t grad(const EmbedGrad &e, hipStream_t s)
+hipError_t grad(EmbedGrad e, hipStream_t s)
 {
     const uint64_t runs = (e.n + e.run - 1) / e.run;
     const uint64_t tiles = (e.n + kEmbedTile - 1) / kEmbedTile;
+    e.scanned = e.n <= kSmallStarts || tiles > kWave;
     if constexpr (F == Form::kRows) {
         if (runs && e.n <= kSmallStarts) {
             embed_starts_small_kernel<<<1, 1024, 0, s>>>(e.keys, (uint32_t)e.n, (uint32_t)e.vocab,
-                                                         e.run, e.starts, e.tiles);
+                                                         e.run, e.starts, e.tiles, e.count);
         } else {
             if (runs)
                 embed_starts_kernel<<<(uint32_t)tiles, 256, 0, s>>>(
                     e.keys, (uint32_t)e.n, (uint32_t)e.vocab, e.run, e.starts, e.tiles);
-            embed_scan_kernel<<<1, kScanThreads, 0, s>>>(runs ? e.tiles : (uint32_t *)e.count, tiles);
+            if (!runs || tiles > kWave)
+                embed_scan_kernel<<<1, kScanThreads, 0, s>>>(runs ? e.tiles : (uint32_t *)e.count,
+                                                             tiles, runs ? e.count : nullptr);
         }
         if (!runs)
             return hipGetLastError();
@@ -861,7 +902,7 @@ hipError_t grad(const EmbedGrad &e, hipStream_t s)
     if (runs > 1) {
         const dim3 grid((uint32_t)((runs + kJoinRuns - 1) / kJoinRuns),
                         (uint32_t)((e.dim + 4 * kWave - 1) / (4 * kWave)));
-        embed_join_kernel<F><<<grid, kJoinThreads, 0, s>>>(e, runs);
+        embed_join_kernel<F><<<grid, kJoinThreads, 0, s>>>(e);
     }
     return hipGetLastError();
 }
@@ -869,11 +910,11 @@ hipError_t grad(const EmbedGrad &e, hipStream_t s)
 uint64_t up256(uint64_t x) { return (x + 255) / 256 * 256; }
 
 // Sorted positions per run: kEmbedRun, or fewer (8 at least) while the runs
-// are too few to give the device 8192 wavefronts of 256 columns.
+// are too few to give the device 4096 wavefronts of 256 columns.
 uint32_t run_length(uint64_t n, uint64_t dim)
 {
     uint32_t r = kEmbedRun;
-    while (r > 8 && (n + r - 1) / r * ((dim + 255) / 256) < 8192)
+    while (r > 8 && (n + r - 1) / r * ((dim + 255) / 256) < 4096)
         r /= 2;
     return r;
 }
