@@ -660,6 +660,7 @@ def embed_lookup(table, tokens, scale: float = 1.0, out=None):
         raise ValueError("table must be a matrix")
     vocab, dim = table.shape
     ld = _matrix(table, "table", vocab, dim, dev)
+    _on(tokens, "tokens", dev)
     n = tokens.numel()
     _vector(tokens, "tokens", n, dev)
     if out is None:
@@ -683,8 +684,8 @@ def embed_sort(tokens, vocab: int, plan=None) -> EmbedPlan:
     """The plan of a batch's tokens for embed_grad and embed_grad_rows.  A
     plan of as many tokens is overwritten if given."""
     lib, torch = _lm(), _torch
-    n = tokens.numel()
     dev = _on(tokens, "tokens")
+    n = tokens.numel()
     _vector(tokens, "tokens", n, dev)
     if plan is None:
         plan = EmbedPlan(torch.empty(lib.embed_plan_words(n), dtype=torch.int32,
@@ -698,9 +699,16 @@ def embed_sort(tokens, vocab: int, plan=None) -> EmbedPlan:
     return plan
 
 
-def _embed_grad_args(lib, grad, plan, dim, work):
+def _embed_grad_args(lib, grad, plan, work):
+    """The checks embed_grad and embed_grad_rows share; (device, row length,
+    distance of the gradient's rows, workspace)."""
     torch = _torch
     dev = _on(grad, "grad")
+    if not isinstance(plan, EmbedPlan):
+        raise TypeError("plan must be an EmbedPlan (embed_sort)")
+    if grad.dim() != 2:
+        raise ValueError("grad must be a matrix")
+    dim = grad.shape[1]
     ld = _matrix(grad, "grad", plan.n, dim, dev)
     _vector(plan.words, "plan", lib.embed_plan_words(plan.n), dev, torch.int32, at_least=True)
     need = lib.embed_work_bytes(plan.n, dim)
@@ -708,7 +716,7 @@ def _embed_grad_args(lib, grad, plan, dim, work):
         work = torch.empty(need, dtype=torch.uint8, device=grad.device)
     else:
         _vector(work, "work", need, dev, torch.uint8, at_least=True)
-    return dev, ld, work
+    return dev, dim, ld, work
 
 
 def embed_grad(grad, plan: EmbedPlan, scale: float = 1.0, out=None, accumulate: bool = False,
@@ -717,8 +725,7 @@ def embed_grad(grad, plan: EmbedPlan, scale: float = 1.0, out=None, accumulate: 
     the positions i of token v), zero where no token is; with ``accumulate``
     it is added to out instead."""
     lib, torch = _lm(), _torch
-    dim = grad.shape[-1]
-    dev, ld, work = _embed_grad_args(lib, grad, plan, dim, work)
+    dev, dim, ld, work = _embed_grad_args(lib, grad, plan, work)
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -738,8 +745,7 @@ def embed_grad_rows(grad, plan: EmbedPlan, scale: float = 1.0, ids=None, rows=No
     ascending order and the same rows their gradients; what is behind them is
     left as it was.  ids and rows hold at least min(n, vocab) entries."""
     lib, torch = _lm(), _torch
-    dim = grad.shape[-1]
-    dev, ld, work = _embed_grad_args(lib, grad, plan, dim, work)
+    dev, dim, ld, work = _embed_grad_args(lib, grad, plan, work)
     most = min(plan.n, plan.vocab)
     if ids is None:
         ids = torch.empty(most, dtype=torch.int32, device=grad.device)
@@ -880,6 +886,7 @@ def _distill_args(logits, index, teacher, temperature, row_scale, scale):
     rows, vocab = logits.shape
     kind = _type_code(logits, "logits")
     ld = _matrix(logits, "logits", rows, vocab, dev)
+    _on(index, "index", dev)
     k = index.shape[-1] if index.dim() else 0
     idx_ld = _matrix(index, "index", rows, k, dev)
     top_ld = _matrix(teacher, "teacher", rows, k, dev)

@@ -90,6 +90,8 @@ def test_binding_refuses_host_tensors():
         gcq.embed_sort(i, 4)
     with pytest.raises(TypeError):
         gcq.embed_lookup([1.0], i)
+    with pytest.raises(TypeError):
+        gcq.embed_sort([1, 2], 4)
     plan = gcq.EmbedPlan(torch.zeros(16, dtype=torch.int32), 4, 4)
     with pytest.raises(ValueError):
         gcq.embed_grad(t, plan)
