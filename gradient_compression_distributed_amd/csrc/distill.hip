@@ -76,8 +76,46 @@ __device__ __forceinline__ void add_logits(Sum &a, const fvec<N> (&z)[U], float 
     a = {m, s};
 }
 
-// Vectors that a lane has in flight.
+// Vectors that a lane has in flight: a batch.
 constexpr int kFlight = 4;
+template <typename T>
+using Batch = vec<T, kVec<T>>[kFlight];
+
+// The thread's vectors of a batch at its column `at`, a workgroup's width
+// apart, all of them inside the row.
+template <typename T, int Threads, bool Nt>
+__device__ __forceinline__ void load_batch(Batch<T> &v, const T *z, uint64_t at)
+{
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+        v[u] = dev::ld<Nt>((const GCQ_G vec<T, kVec<T>> *)(z + at + u * Threads * kVec<T>));
+}
+
+template <typename T>
+__device__ __forceinline__ void add_batch(Sum &a, const Batch<T> &v, float c)
+{
+    fvec<kVec<T>> f[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+        f[u] = to_f32<T, kVec<T>>(v[u]);
+    add_logits<kFlight, kVec<T>>(a, f, c);
+}
+
+// dz = value(z) for a batch.  Non-temporal: dz is not read here, so the rows
+// still to be read keep the caches.
+template <typename T, int Threads, typename F>
+__device__ __forceinline__ void put_batch(T *dz, const Batch<T> &v, uint64_t at, F value)
+{
+    constexpr int N = kVec<T>;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+        fvec<N> f = to_f32<T, N>(v[u]);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            f[j] = value(f[j]);
+        dev::st<true>((GCQ_G vec<T, N> *)(dz + at + u * Threads * N), from_f32<T, N>(f));
+    }
+}
 
 // Adds columns [c0, c1) of a row, a share of them per thread.  Nt: the row is
 // not read again (2048 x 131072 bf16, loss alone: 80 us, else 85).
@@ -88,15 +126,9 @@ __device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_
     constexpr uint64_t step = (uint64_t)Threads * N;
     uint64_t at = c0 + (uint64_t)threadIdx.x * N;
     for (; at + (U - 1) * step + N <= c1; at += U * step) {
-        vec<T, N> v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            v[u] = dev::ld<Nt>((const GCQ_G vec<T, N> *)(z + at + u * step));
-        fvec<N> f[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            f[u] = to_f32<T, N>(v[u]);
-        add_logits<U, N>(a, f, c);
+        Batch<T> v;
+        load_batch<T, Threads, Nt>(v, z, at);
+        add_batch<T>(a, v, c);
     }
     for (; at < c1; at += step) {
         const int64_t left = (int64_t)(c1 - at);
@@ -108,10 +140,9 @@ __device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_
     }
 }
 
-// dz = value(z) over columns [c0, c1).  Non-temporal on both sides: the
-// logits are read for the last time and dz is not read here, so the rows
-// still to be read keep the caches (2048 x 131072 bf16 from a kept lse: 175
-// us, with ordinary loads 195).
+// dz = value(z) over columns [c0, c1).  The logits are read for the last time,
+// so non-temporally too (2048 x 131072 bf16 from a kept lse: 175 us, with
+// ordinary loads 195).
 template <typename T, int Threads, typename F>
 __device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t c1, F value)
 {
@@ -119,18 +150,9 @@ __device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t
     constexpr uint64_t step = (uint64_t)Threads * N;
     uint64_t at = c0 + (uint64_t)threadIdx.x * N;
     for (; at + (U - 1) * step + N <= c1; at += U * step) {
-        vec<T, N> v[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            v[u] = dev::ld<true>((const GCQ_G vec<T, N> *)(z + at + u * step));
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            fvec<N> f = to_f32<T, N>(v[u]);
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                f[j] = value(f[j]);
-            dev::st<true>((GCQ_G vec<T, N> *)(dz + at + u * step), from_f32<T, N>(f));
-        }
+        Batch<T> v;
+        load_batch<T, Threads, true>(v, z, at);
+        put_batch<T, Threads>(dz, v, at, value);
     }
     for (; at < c1; at += step) {
         const int64_t left = (int64_t)(c1 - at);
@@ -152,6 +174,9 @@ __device__ __forceinline__ void zero_row(T *dz, uint64_t c0, uint64_t c1)
 }
 
 constexpr uint32_t kNone = 0xFFFFFFFFu;
+
+// LDS of a row's entries, a multiple of 16 bytes.
+__host__ __device__ constexpr uint32_t entry_bytes(uint32_t k) { return (12 * k + 15) / 16 * 16; }
 
 template <typename T>
 __device__ __forceinline__ float teacher_logit(const Distill &a, uint64_t row, uint32_t j)
@@ -283,12 +308,20 @@ __device__ __forceinline__ float reduce_get(const float *part)
 }
 
 // Loss and lse, and with Grad dz too: a workgroup per row.  The entries'
-// loads travel while the row is summed; the second pass finds what it reads
-// again in the caches.
+// loads travel while the row is summed.  Both passes together read the row
+// twice and write it once, and all of that goes through the fabric between
+// the compute units and the last cache, which bounds the call (3 GB at 7 TB/s
+// for 4096 x 131072 bf16; without the exponentials it took as long).  So the
+// row's first `kept` batches stay in LDS, each thread's own vectors: 423 ->
+// 393 us there, 8192 x 65536 395 -> 368.
 template <typename T, int Threads, bool Grad>
-__global__ __launch_bounds__(Threads) void distill_loss_kernel(Distill a)
+__global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uint32_t kept)
 {
-    constexpr int N = kVec<T>, Waves = Threads / kWave;
+    using Stash = uint32_t __attribute__((ext_vector_type(4)));
+    using Packed = T __attribute__((ext_vector_type(kVec<T>)));
+    constexpr int Waves = Threads / kWave;
+    constexpr uint64_t width = (uint64_t)Threads * kVec<T> * kFlight;
+    const uint64_t first = threadIdx.x * kVec<T>;
     extern __shared__ __align__(16) uint32_t lds[];
     __shared__ Sum sum_s[Waves];
     __shared__ float top_s[Waves], red_s[3][Waves];
@@ -312,10 +345,21 @@ __global__ __launch_bounds__(Threads) void distill_loss_kernel(Distill a)
     e.own = load_entry<T>(a, row, tid);
     const float c = kLog2e / a.temp;
     Sum r = {kLowest, 0.0f};
-    const uint64_t half = a.vocab / (2 * Threads * N) * (Threads * N);
-    add_row<T, Threads, !Grad>(r, z, 0, half, c);
+    Stash *stash = (Stash *)((char *)lds + entry_bytes(a.k));   // [batches][kFlight][Threads]
+    for (uint32_t b = 0; b < kept; ++b) {
+        Batch<T> v;
+        load_batch<T, Threads, true>(v, z, first + b * width);
+        add_batch<T>(r, v, c);
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u)
+            stash[(b * kFlight + u) * Threads + tid] = __builtin_bit_cast(Stash, (Packed)v[u]);
+    }
+    // the entries' columns have arrived by the row's middle
+    constexpr uint64_t step = width / kFlight;
+    const uint64_t half = a.vocab / (2 * step) * step, mid = kept ? kept * width : half;
+    add_row<T, Threads, !Grad>(r, z, kept * width, mid, c);
     e.read_logits(a, row, z, 0, a.vocab);
-    add_row<T, Threads, !Grad>(r, z, half, a.vocab, c);
+    add_row<T, Threads, !Grad>(r, z, mid, a.vocab, c);
     r = join_lanes<kWave>(r, c);
     if ((tid & (kWave - 1)) == 0)
         sum_s[tid / kWave] = r;
@@ -349,8 +393,15 @@ __global__ __launch_bounds__(Threads) void distill_loss_kernel(Distill a)
             return;
         }
         const float g = s / a.temp, inv = 1.0f / r.s, f = g / r.s;
-        map_row<T, Threads>(z, dz, 0, a.vocab,
-                               [=](float x) { return exp2_hw((x - r.m) * c) * f; });
+        const auto value = [=](float x) { return exp2_hw((x - r.m) * c) * f; };
+        for (uint32_t b = 0; b < kept; ++b) {
+            Batch<T> v;
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u)
+                v[u] = __builtin_bit_cast(Packed, stash[(b * kFlight + u) * Threads + tid]);
+            put_batch<T, Threads>(dz, v, first + b * width, value);
+        }
+        map_row<T, Threads>(z, dz, kept * width, a.vocab, value);
         __syncthreads();
         e.put(a, dz, 0, a.vocab, g, w[0],
               [=](float x) { return exp2_hw((x - r.m) * c) * inv; });
@@ -408,18 +459,30 @@ __global__ __launch_bounds__(Threads) void distill_grad_kernel(Distill a, uint64
 template <typename T, int Threads>
 void loss(const Distill &a, hipStream_t s)
 {
-    if (a.dz)
-        distill_loss_kernel<T, Threads, true><<<block_grid(a.rows), Threads, 12 * a.k, s>>>(a);
-    else
-        distill_loss_kernel<T, Threads, false><<<block_grid(a.rows), Threads, 12 * a.k, s>>>(a);
+    const uint32_t lds = entry_bytes(a.k);
+    if (a.dz) {
+        // batches that fit the workgroup's share of a compute unit's LDS
+        const uint32_t batch = Threads * 16 * kFlight;
+        const uint32_t share = dev::kLdsBytesPerCu / (2048 / Threads) - 512u;
+        const uint64_t all = a.vocab * sizeof(T) / batch;
+        uint32_t kept = lds < share ? (share - lds) / batch : 0;
+        kept = all < kept ? (uint32_t)all : kept;
+        distill_loss_kernel<T, Threads, true>
+            <<<block_grid(a.rows), Threads, lds + kept * batch, s>>>(a, kept);
+    } else {
+        distill_loss_kernel<T, Threads, false><<<block_grid(a.rows), Threads, lds, s>>>(a, 0);
+    }
 }
 
 template <typename T>
 hipError_t loss(const Distill &a, hipStream_t s)
 {
-    // threads for one pass of a few vectors each, U in flight; rows of 8192 x
-    // 131072 bytes and more in flight at once no longer stay in the caches
-    // between the two passes, so long rows get few, large workgroups
+    // A workgroup for a few vectors a lane.  Long rows get few, large
+    // workgroups: with many rows in flight at once they no longer stay in the
+    // caches between the two passes.  Loss and gradient in bf16, us with 64 /
+    // 256 / 512 / 1024 threads: 8192 x 1000 19 / 32 / 57 / 146; 8192 x 8000 83
+    // / 75 / 90 / 169; 8192 x 32000 300 / 242 / 224 / 278; 4096 x 131072 633 /
+    // 579 / 486 / 437.
     const uint64_t bytes = a.vocab * sizeof(T);
     if (bytes <= 8192)
         loss<T, 64>(a, s);
@@ -439,7 +502,7 @@ hipError_t grad(const Distill &a, hipStream_t s)
     const uint64_t chunk = (uint64_t)threads * kVec<T> * 8;
     const uint64_t parts = (a.vocab + chunk - 1) / chunk;
     distill_grad_kernel<T, threads>
-        <<<block_grid(a.rows * parts), threads, 12 * a.k, s>>>(a, parts, chunk);
+        <<<block_grid(a.rows * parts), threads, entry_bytes(a.k), s>>>(a, parts, chunk);
     return hipGetLastError();
 }
 
