@@ -411,7 +411,8 @@ __global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uin
 // dz from a kept lse; `parts` workgroups share a row, `chunk` columns each.
 // The exponent is ((z - hi) - lo) log2(e) / T with hi + lo = lse T: exact
 // where q is large.  Whether the row has entries at all is known only after
-// the dense pass; a row without is zeroed then.
+// the dense pass; a row without is zeroed then.  Bound by memory: 2048 x 131072
+// bf16 178 us (1.02 GB, 5.7 TB/s).
 template <typename T, int Threads>
 __global__ __launch_bounds__(Threads) void distill_grad_kernel(Distill a, uint64_t parts,
                                                                uint64_t chunk)

@@ -23,7 +23,9 @@ using namespace lm;
 // L lanes share a row (a power of two up to 256), so a workgroup of 256
 // threads copies 256 / L rows at once, R times over.  The R tokens are loaded
 // together and then the R rows' vectors, so a row waits for one load, not for
-// two in turn.
+// two in turn (32768 rows of 4096 bf16, us for R = 1 / 2 / 4 / 8: 80 / 75 / 82 /
+// 83).  Bound by the fabric: rows of frequent tokens come from the last cache,
+// 268 MB out and as much in at 7.2 TB/s.  A few rows take a launch (3 us).
 template <typename T, typename O>
 constexpr int kLookup = kVec<T> < kVec<O> ? kVec<T> : kVec<O>;   // 16 bytes at most on either side
 
@@ -78,7 +80,10 @@ __device__ __forceinline__ uint32_t key_of(int64_t token, uint64_t vocab)
 // behind it with a smaller key.  A workgroup holds every key in LDS; Ti lanes
 // take a position each, 1024 / Ti groups of lanes a share of the others.
 // n^2 comparisons (2 instructions each) cost less than the passes of a radix
-// sort, each of them bound by launch and latency, up to kCountSort positions.
+// sort, each of them bound by launch and latency, up to kCountSort positions:
+// 7 us at 4000; with the rest of a row-sparse gradient of 64 columns 31 us
+// against 40 at 6000 and 34 against 40 at 8000, but 38 us against 26 for the
+// sort alone at 16384.
 constexpr uint32_t kCountSort = 8192;
 template <typename I, uint32_t Ti>
 __global__ __launch_bounds__(1024) void embed_count_sort_kernel(const I *__restrict__ tokens,
@@ -124,7 +129,9 @@ __global__ __launch_bounds__(1024) void embed_count_sort_kernel(const I *__restr
 // most 9 bits, tiles of 2048 positions, two launches a pass.  A wavefront
 // ranks 64 keys at a time: a ballot per digit bit gives each lane the lanes
 // that share its digit, so the rank is a count of lower lanes plus the
-// wavefront's count so far, and equal digits keep their order.
+// wavefront's count so far, and equal digits keep their order.  65536 tokens
+// of 18 bits: 24 us in four launches of 5 to 7, each a few dependent trips to
+// memory that another launch wrote.
 constexpr uint32_t kDigitBits = 9, kBins = 1u << kDigitBits;
 constexpr uint32_t kSortThreads = 512, kSortItems = 4;
 constexpr uint32_t kSortTile = kSortThreads * kSortItems;
@@ -554,7 +561,14 @@ __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64
 // loads and every branch on them is uniform.  A segment inside the run is
 // finished here; one that reaches over an end leaves its sum in part[run][0]
 // (it began before the run) or part[run][1].  kWrite: the workgroups behind
-// the first `blocks` zero the rows that no position names.
+// the first `blocks` zero the rows that no position names, in pieces of 64 KiB
+// (50021 x 1001 float32, all in all: 62 us; 16 KiB 64.5, 256 KiB 62).
+//
+// Bound by memory: 65536 x 2048 bf16 into 20000 rows moves 445 MB in 87 us (5.1
+// TB/s), 16384 x 4096 bf16 added to a 2 GiB table 366 MB in 76 us (4.8 TB/s,
+// reads and writes of scattered rows); a copy of that size reaches 5.4.
+// Prefetching the next batch, other batches and longer or shorter runs changed
+// nothing.
 template <typename T, Form F>
 __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t cols,
                                                          uint64_t blocks, uint32_t span)
@@ -615,7 +629,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t c
                     v[j] = load_vec<T, N, true>(g + pos[j] * e.ld, left);
                 if constexpr (F == Form::kAdd)
                     if (key[j] != key[j + 1] && left > 0)
-                        old[j] = load_vec<float, N, true>(e.out + key[j] * e.out_ld + c, left);
+                        old[j] = load_vec<float, N>(e.out + key[j] * e.out_ld + c, left);
             }
         }
 #pragma unroll
