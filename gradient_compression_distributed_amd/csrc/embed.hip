@@ -92,7 +92,8 @@ __global__ __launch_bounds__(1024) void embed_count_sort_kernel(const I *__restr
                                                                 uint32_t *__restrict__ keys,
                                                                 uint32_t *__restrict__ order)
 {
-    extern __shared__ __align__(16) uint32_t key_s[];   // share * 1024 / Ti keys, those past n never counted
+    // share * 1024 / Ti keys, those past n never counted
+    extern __shared__ __align__(16) uint32_t key_s[];
     __shared__ uint32_t place[Ti];
     const uint32_t tid = threadIdx.x, all = share * (1024u / Ti);
     for (uint32_t j = tid; j < all; j += 1024u)
@@ -544,14 +545,14 @@ __device__ __forceinline__ void zero_rows(const EmbedGrad &e, uint64_t v0, uint3
 }
 
 // Where a finished sum goes; `old` is what is there (kAdd).
-template <Form F, int N>
+template <Form F, int N, bool Nt>
 __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64_t c,
                                         fvec<N> acc, fvec<N> old, int64_t left)
 {
     fvec<N> v = acc * e.scale;
     if constexpr (F == Form::kAdd)
         v += old;
-    store_vec<float, N, true>(e.out + row * e.out_ld + c, v, left);
+    store_vec<float, N, Nt>(e.out + row * e.out_ld + c, v, left);
 }
 
 // One pass over g in sorted order.  A wavefront takes a run of e.run sorted
@@ -568,8 +569,10 @@ __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64
 // TB/s), 16384 x 4096 bf16 added to a 2 GiB table 366 MB in 76 us (4.8 TB/s,
 // reads and writes of scattered rows); a copy of that size reaches 5.4.
 // Prefetching the next batch, other batches and longer or shorter runs changed
-// nothing.
-template <typename T, Form F>
+// nothing.  Nt: the gradient is read and the sums stored non-temporally, from
+// 32 MiB of gradient on (the last case: 102 us, with ordinary accesses 110; but
+// 4001 x 1001 float32 61 against 58.5, as smaller ones are still in the caches).
+template <typename T, Form F, bool Nt>
 __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t cols,
                                                          uint64_t blocks, uint32_t span)
 {
@@ -596,11 +599,10 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t c
     const int64_t left = c < e.dim ? (int64_t)(e.dim - c) : 0;
     const T *g = (const T *)e.g + c;
     uint64_t seat = 0;
-    if constexpr (F == Form::kRows)
+    if constexpr (F == Form::kRows) {
         seat = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane(
                    (int)starts_before(e, i0 / kEmbedTile)) +
                ((Scalar *)e.starts)[run] - 1u;   // of the segment open here
-    if constexpr (F == Form::kRows) {
         if (item == 0 && !e.scanned) {
             const uint32_t all = starts_before(e, (n + kEmbedTile - 1) / kEmbedTile);
             if (lane == 0)
@@ -626,7 +628,7 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t c
             old[j] = 0.0f;
             if (key[j] < e.vocab && pos[j] < n) {   // padding is not read
                 if (left > 0)
-                    v[j] = load_vec<T, N, true>(g + pos[j] * e.ld, left);
+                    v[j] = load_vec<T, N, Nt>(g + pos[j] * e.ld, left);
                 if constexpr (F == Form::kAdd)
                     if (key[j] != key[j + 1] && left > 0)
                         old[j] = load_vec<float, N>(e.out + key[j] * e.out_ld + c, left);
@@ -655,7 +657,8 @@ __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t c
                     if (head)
                         store_vec<float, N>(e.part + 2 * run * e.dim + c, acc, left);
                     else
-                        put_row<F, N>(e, F == Form::kRows ? seat : k, c, acc, old[j], left);
+                        put_row<F, N, Nt>(e, F == Form::kRows ? seat : k, c, acc, old[j],
+                                          left);
                 }
             } else if (b + j + 1 == end && left > 0) {
                 store_vec<float, N>(e.part + (2 * run + (head ? 0 : 1)) * e.dim + c, acc, left);
@@ -766,7 +769,7 @@ __global__ __launch_bounds__(kJoinThreads) void embed_join_kernel(EmbedGrad e)
             row = (uint64_t)(e.scanned ? before : sum_counts(before)) + starts + opens - 1u;
         }
         if (left > 0 && (alone || lane < 8u))
-            put_row<F, N>(e, row, c, acc, old, left);
+            put_row<F, N, false>(e, row, c, acc, old, left);
     }
 }
 
@@ -785,12 +788,10 @@ hipError_t lookup(const EmbedTable &t, const void *tokens, uint64_t n, float sca
 {
     const uint32_t lanes = lanes_for(t.dim, kLookup<T, O>);
     const uint64_t per = 256u / lanes, blocks = (n + per - 1) / per;
-    if (blocks >= 4096)
-        embed_lookup_kernel<T, O, I, 2><<<block_grid((blocks + 1) / 2), 256, 0, s>>>(
-            (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
-    else
-        embed_lookup_kernel<T, O, I, 1><<<block_grid(blocks), 256, 0, s>>>(
-            (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
+    const auto kernel = blocks >= 4096 ? embed_lookup_kernel<T, O, I, 2>
+                                       : embed_lookup_kernel<T, O, I, 1>;
+    kernel<<<block_grid(blocks >= 4096 ? (blocks + 1) / 2 : blocks), 256, 0, s>>>(
+        (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
     return hipGetLastError();
 }
 
@@ -884,7 +885,11 @@ void sum_runs(const EmbedGrad &e, uint64_t runs, hipStream_t s)
     // rows that a zeroing workgroup looks at: about 64 KiB, 64 at most
     const uint32_t span = (uint32_t)(e.dim >= 16384 ? 1u : e.dim <= 256 ? 64u : 16384 / e.dim);
     const uint64_t zero = F == Form::kWrite ? (e.vocab + span - 1) / span : 0;
-    embed_grad_kernel<T, F><<<block_grid(blocks + zero), 256, 0, s>>>(e, cols, blocks, span);
+    const dim3 grid = block_grid(blocks + zero);
+    if (e.n * e.dim * sizeof(T) >= (32ull << 20))
+        embed_grad_kernel<T, F, true><<<grid, 256, 0, s>>>(e, cols, blocks, span);
+    else
+        embed_grad_kernel<T, F, false><<<grid, 256, 0, s>>>(e, cols, blocks, span);
 }
 
 template <Form F>

@@ -339,9 +339,9 @@ int distill(const void *z, int type, size_t rows, size_t vocab, size_t z_ld, con
     if (!z || !idx || !top || (loss_wanted ? !loss || !lse_out : !lse_in) || (grad_wanted && !dz))
         return GCQ_ERR_NULL;
     const size_t es = type_bytes(type);
-    if (!aligned(z, es) || !aligned(idx, type_bytes(idx_type)) || !aligned(top, type_bytes(top_type)) ||
-        !aligned(row_scale, 4) || !aligned(lse_in, 4) || !aligned(loss, 4) || !aligned(lse_out, 4) ||
-        !aligned(dz, es))
+    if (!aligned(z, es) || !aligned(idx, type_bytes(idx_type)) ||
+        !aligned(top, type_bytes(top_type)) || !aligned(row_scale, 4) || !aligned(lse_in, 4) ||
+        !aligned(loss, 4) || !aligned(lse_out, 4) || !aligned(dz, es))
         return GCQ_ERR_ALIGN;
     Range r[8];
     int n = 0;
