@@ -117,8 +117,12 @@ __device__ __forceinline__ void put_batch(T *dz, const Batch<T> &v, uint64_t at,
     }
 }
 
-// Adds columns [c0, c1) of a row, a share of them per thread.  Nt: the row is
-// not read again (2048 x 131072 bf16, loss alone: 80 us, else 85).
+// Non-temporal loads of logits that are read once (Nt): from 96 MiB on they
+// pay (2048 x 131072 bf16, loss 80 us against 85, gradient from a kept lse 175
+// against 195; at 1024 x 32000, 62 MiB, 15.5 against 15.0 and 29 against 24.5).
+constexpr uint64_t kStreamBytes = 96ull << 20;
+
+// Adds columns [c0, c1) of a row, a share of them per thread.
 template <typename T, int Threads, bool Nt>
 __device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_t c1, float c)
 {
@@ -140,10 +144,8 @@ __device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_
     }
 }
 
-// dz = value(z) over columns [c0, c1).  The logits are read for the last time,
-// so non-temporally too (2048 x 131072 bf16 from a kept lse: 175 us, with
-// ordinary loads 195).
-template <typename T, int Threads, typename F>
+// dz = value(z) over columns [c0, c1).
+template <typename T, int Threads, bool Nt, typename F>
 __device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t c1, F value)
 {
     constexpr int N = kVec<T>, U = kFlight;
@@ -151,7 +153,7 @@ __device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t
     uint64_t at = c0 + (uint64_t)threadIdx.x * N;
     for (; at + (U - 1) * step + N <= c1; at += U * step) {
         Batch<T> v;
-        load_batch<T, Threads, true>(v, z, at);
+        load_batch<T, Threads, Nt>(v, z, at);
         put_batch<T, Threads>(dz, v, at, value);
     }
     for (; at < c1; at += step) {
@@ -314,7 +316,7 @@ __device__ __forceinline__ float reduce_get(const float *part)
 // for 4096 x 131072 bf16; without the exponentials it took as long).  So the
 // row's first `kept` batches stay in LDS, each thread's own vectors: 423 ->
 // 393 us there, 8192 x 65536 395 -> 368.
-template <typename T, int Threads, bool Grad>
+template <typename T, int Threads, bool Grad, bool Nt>
 __global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uint32_t kept)
 {
     using Stash = uint32_t __attribute__((ext_vector_type(4)));
@@ -357,9 +359,9 @@ __global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uin
     // the entries' columns have arrived by the row's middle
     constexpr uint64_t step = width / kFlight;
     const uint64_t half = a.vocab / (2 * step) * step, mid = kept ? kept * width : half;
-    add_row<T, Threads, !Grad>(r, z, kept * width, mid, c);
+    add_row<T, Threads, Nt>(r, z, kept * width, mid, c);
     e.read_logits(a, row, z, 0, a.vocab);
-    add_row<T, Threads, !Grad>(r, z, mid, a.vocab, c);
+    add_row<T, Threads, Nt>(r, z, mid, a.vocab, c);
     r = join_lanes<kWave>(r, c);
     if ((tid & (kWave - 1)) == 0)
         sum_s[tid / kWave] = r;
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uin
                 v[u] = __builtin_bit_cast(Packed, stash[(b * kFlight + u) * Threads + tid]);
             put_batch<T, Threads>(dz, v, first + b * width, value);
         }
-        map_row<T, Threads>(z, dz, kept * width, a.vocab, value);
+        map_row<T, Threads, true>(z, dz, kept * width, a.vocab, value);
         __syncthreads();
         e.put(a, dz, 0, a.vocab, g, w[0],
               [=](float x) { return exp2_hw((x - r.m) * c) * inv; });
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uin
 // where q is large.  Whether the row has entries at all is known only after
 // the dense pass; a row without is zeroed then.  Bound by memory: 2048 x 131072
 // bf16 178 us (1.02 GB, 5.7 TB/s).
-template <typename T, int Threads>
+template <typename T, int Threads, bool Nt>
 __global__ __launch_bounds__(Threads) void distill_grad_kernel(Distill a, uint64_t parts,
                                                                uint64_t chunk)
 {
@@ -440,7 +442,7 @@ __global__ __launch_bounds__(Threads) void distill_grad_kernel(Distill a, uint64
     const float c = kLog2e / a.temp, g = s / a.temp;
     const float hi = lse * a.temp, lo = fmaf(lse, a.temp, -hi);
     const auto q = [=](float x) { return exp2_hw(((x - hi) - lo) * c); };
-    map_row<T, Threads>(z, dz, c0, c1, [=](float x) { return q(x) * g; });
+    map_row<T, Threads, Nt>(z, dz, c0, c1, [=](float x) { return q(x) * g; });
     reduce_put<Waves, true>(e.top(a), top_s);
     __syncthreads();
     float tm = reduce_get<Waves, true>(top_s);
@@ -468,10 +470,13 @@ void loss(const Distill &a, hipStream_t s)
         const uint64_t all = a.vocab * sizeof(T) / batch;
         uint32_t kept = lds < share ? (share - lds) / batch : 0;
         kept = all < kept ? (uint32_t)all : kept;
-        distill_loss_kernel<T, Threads, true>
+        distill_loss_kernel<T, Threads, true, false>
             <<<block_grid(a.rows), Threads, lds + kept * batch, s>>>(a, kept);
     } else {
-        distill_loss_kernel<T, Threads, false><<<block_grid(a.rows), Threads, lds, s>>>(a, 0);
+        const auto kernel = a.rows * a.vocab * sizeof(T) >= kStreamBytes
+                                ? distill_loss_kernel<T, Threads, false, true>
+                                : distill_loss_kernel<T, Threads, false, false>;
+        kernel<<<block_grid(a.rows), Threads, lds, s>>>(a, 0);
     }
 }
 
@@ -502,8 +507,10 @@ hipError_t grad(const Distill &a, hipStream_t s)
     constexpr int threads = 256;
     const uint64_t chunk = (uint64_t)threads * kVec<T> * 8;
     const uint64_t parts = (a.vocab + chunk - 1) / chunk;
-    distill_grad_kernel<T, threads>
-        <<<block_grid(a.rows * parts), threads, entry_bytes(a.k), s>>>(a, parts, chunk);
+    const auto kernel = a.rows * a.vocab * sizeof(T) >= kStreamBytes
+                            ? distill_grad_kernel<T, threads, true>
+                            : distill_grad_kernel<T, threads, false>;
+    kernel<<<block_grid(a.rows * parts), threads, entry_bytes(a.k), s>>>(a, parts, chunk);
     return hipGetLastError();
 }
 

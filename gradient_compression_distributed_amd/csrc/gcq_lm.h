@@ -128,8 +128,8 @@ struct EmbedGrad {
     bool add;                       // dense: add to out; else overwrite
     uint32_t run;                   // sorted positions per run
     uint32_t *starts;               // workspace: segment starts before each run, in its tile
-    uint32_t *tiles;                // workspace: segment starts in each tile, or (scanned) before it
-    bool scanned;
+    uint32_t *tiles;                // workspace: segment starts in each tile, or before it ...
+    bool scanned;                   // ... (scanned)
     float *part;                    // workspace: [runs][2][dim] open sums
 };
 

@@ -251,8 +251,9 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNorm a)
 // A slot is the L lanes that share a row; slot s takes rows s, s + slots, ...
 // and keeps its share of dw in registers, written to part_w[s] at the end, so
 // dy, h and dh are read once for both gradients.  Bound by memory: 16384 x 4096
-// bf16 94 us of 100 (537 MB, 5.7 TB/s), the rest joins the shares.
-template <typename T, int L, int Ch>
+// bf16 94 us of 100 (537 MB, 5.7 TB/s), the rest joins the shares.  Nt: the
+// matrices by non-temporal accesses.
+template <typename T, int L, int Ch, bool Nt>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_grad_kernel(RmsGrad a)
 {
     constexpr int N = kVec<T>, Threads = L < 256 ? 256 : L;
@@ -278,10 +279,10 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_grad_kernel(RmsGra
             gv[i] = hv[i] = dv[i] = (T)0.0f;
             if (c < a.dim) {
                 const int64_t left = (int64_t)(a.dim - c);
-                gv[i] = load_vec<T, N, true>(dy + c, left);
-                hv[i] = load_vec<T, N, true>(h + c, left);
+                gv[i] = load_vec<T, N, Nt>(dy + c, left);
+                hv[i] = load_vec<T, N, Nt>(h + c, left);
                 if (a.dh)
-                    dv[i] = load_vec<T, N, true>(dh + c, left);
+                    dv[i] = load_vec<T, N, Nt>(dh + c, left);
             }
         }
 #pragma unroll
@@ -311,7 +312,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_grad_kernel(RmsGra
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 d[j] = fmaf(rstd, fmaf(-hf[j], k, g[j] * w[j]), d[j]);
-            store_vec<T, N, true>((T *)a.dx + row * a.dx_ld + c, from_f32<T, N>(d), left);
+            store_vec<T, N, Nt>((T *)a.dx + row * a.dx_ld + c, from_f32<T, N>(d), left);
         }
     }
 #pragma unroll
@@ -477,17 +478,28 @@ uint64_t grad_slots(uint64_t rows, int lanes)
     return rows < most ? rows : most;
 }
 
-template <typename T, int L>
-void norm_grad(const RmsGrad &a, int ch, hipStream_t s)
+template <typename T, int L, int Ch>
+void norm_grad(const RmsGrad &a, hipStream_t s)
 {
     constexpr int threads = L < 256 ? 256 : L, per = threads / L;
     const uint32_t grid = (uint32_t)((a.slots + per - 1) / per);
+    // from 64 MiB a matrix on: 16384 x 4096 bf16 101 us against 104, but 2048 x
+    // 4096 (16 MiB) 26 against 21
+    if (a.rows * a.dim * sizeof(T) >= (64ull << 20))
+        rms_norm_grad_kernel<T, L, Ch, true><<<grid, threads, 0, s>>>(a);
+    else
+        rms_norm_grad_kernel<T, L, Ch, false><<<grid, threads, 0, s>>>(a);
+}
+
+template <typename T, int L>
+void norm_grad(const RmsGrad &a, int ch, hipStream_t s)
+{
     if (ch == 1)
-        rms_norm_grad_kernel<T, L, 1><<<grid, threads, 0, s>>>(a);
+        norm_grad<T, L, 1>(a, s);
     else if (ch == 2)
-        rms_norm_grad_kernel<T, L, 2><<<grid, threads, 0, s>>>(a);
+        norm_grad<T, L, 2>(a, s);
     else if constexpr (L == 1024 && sizeof(T) == 4)
-        rms_norm_grad_kernel<T, L, 4><<<grid, threads, 0, s>>>(a);
+        norm_grad<T, L, 4>(a, s);
 }
 
 template <typename T>

@@ -113,6 +113,20 @@ def test_against_plain(gpu, kind, index, T):
         assert torch.equal(gpu.distill_grad(z2, lse, idx, top, T, row_scale, scale, out=z2), dz)
 
 
+@pytest.mark.parametrize("kind", TYPES)
+def test_many_rows(gpu, kind):
+    """Logits past the size from which they are read non-temporally."""
+    import torch
+
+    rows, V = (420, 70001) if kind == "float32" else (800, 70001)
+    z, idx, top, rs = case(11, rows, V, 33, kind, extra=2)
+    want = plain(z, idx, top, 1.5, rs, 3.0)
+    loss, lse = gpu.distill_loss(z, idx, top, 1.5, rs, 3.0)
+    check((loss, lse, None), want, V, kind)
+    check((None, None, gpu.distill_grad(z, lse, idx, top, 1.5, rs, 3.0)), want, V, kind)
+    check(gpu.distill_loss_grad(z, idx, top, 1.5, rs, 3.0), want, V, kind)
+
+
 def test_rows_with_nothing(gpu):
     """No entry, entries of -inf alone, masked rows, logits of -inf or of the
     type's lowest value, and rows that hold NaN but are not read."""

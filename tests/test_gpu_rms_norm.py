@@ -232,6 +232,38 @@ def test_norm_grad(gpu, kind, w32, with_dh):
             assert torch.equal(dx3, dx)
 
 
+# three vectors a lane (64 and 256 lanes), and matrices past the sizes from
+# which accesses are non-temporal
+MANY = [(1030, 700), (1025, 1400), (1025, 2500), (1025, 5000), (9000, 4100)]
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("rows,dim", MANY)
+def test_many_rows(gpu, kind, rows, dim):
+    import torch
+
+    print("[gpu] many rows", kind, rows, dim, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(rows + dim)
+    x, res, dy = (torch.randn(rows, dim, generator=g, device="cuda").to(dtype(kind)) for _ in range(3))
+    w = torch.randn(dim, generator=g, device="cuda")
+    hd, rd, yd = plain(x, w, EPS, res)
+    y, h, rstd = gpu.rms_norm(x, w, EPS, residual=res)
+    near(rstd, rd, few(dim), "rstd")
+    near(h, hd, HALF[kind] + E, "h", tiny(kind))
+    near(y, yd, HALF[kind] + few(dim) + 4 * E, "y", tiny(kind))
+    codes, scales, h8, rstd8 = gpu.rms_norm_q8(x, w, EPS, group=128, residual=res)
+    assert torch.equal(h8, h) and torch.equal(rstd8, rstd)
+    v = codes.float().double() * scales.double()[:, torch.arange(dim, device="cuda") // 128]
+    # half a step of three fraction bits, or of the smallest code
+    least = 2.0 ** -10 * scales.double()[:, torch.arange(dim, device="cuda") // 128]
+    assert ((v - yd).abs() <= (2.0 ** -4 + 3 * few(dim)) * yd.abs() + least).all()
+    dxd, size, dwd, dwsize = plain_grad(dy, h, w, rstd, res)
+    dx, dw = gpu.rms_norm_grad(dy, h, w, rstd, dh=res)
+    off = (dx.double() - dxd).abs()
+    assert (off <= HALF[kind] * dxd.abs() + (few(dim) + 8 * E) * size + tiny(kind)).all()
+    assert ((dw.double() - dwd).abs() <= (rows + 40) * E * dwsize + 1e-44).all()
+
+
 def test_grad_is_the_norms(gpu):
     """Differences of the 64-bit norm along random directions."""
     import torch
