@@ -91,6 +91,25 @@ __device__ __forceinline__ void load_batch(Batch<T> &v, const T *z, uint64_t at)
         v[u] = dev::ld<Nt>((const GCQ_G vec<T, kVec<T>> *)(z + at + u * Threads * kVec<T>));
 }
 
+// Where a thread's vectors of a row wait in LDS between two passes.
+template <typename T>
+using Stash = uint32_t __attribute__((ext_vector_type(4)));
+template <typename T>
+using Packed = T __attribute__((ext_vector_type(kVec<T>)));
+
+// Keeps the compiler from holding a batch converted to 32 bits, in twice the
+// registers, from the first pass to the second.
+template <typename T>
+__device__ __forceinline__ void hide(Batch<T> &v)
+{
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+        Stash<T> x = __builtin_bit_cast(Stash<T>, (Packed<T>)v[u]);
+        asm volatile("" : "+v"(x));
+        v[u] = __builtin_bit_cast(Packed<T>, x);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void add_batch(Sum &a, const Batch<T> &v, float c)
 {
@@ -122,21 +141,35 @@ __device__ __forceinline__ void put_batch(T *dz, const Batch<T> &v, uint64_t at,
 // against 195; at 1024 x 32000, 62 MiB, 15.5 against 15.0 and 29 against 24.5).
 constexpr uint64_t kStreamBytes = 96ull << 20;
 
-// Adds columns [c0, c1) of a row, a share of them per thread.
-template <typename T, int Threads, bool Nt>
-__device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_t c1, float c)
+// Adds columns [c0, c1) of a row, a share of them per thread, and with Keep
+// leaves them in the stash.
+template <typename T, int Threads, bool Nt, bool Keep = false>
+__device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_t c1, float c,
+                                        Stash<T> *stash = nullptr)
 {
     constexpr int N = kVec<T>, U = kFlight;
     constexpr uint64_t step = (uint64_t)Threads * N;
     uint64_t at = c0 + (uint64_t)threadIdx.x * N;
+    uint32_t slot = threadIdx.x;
     for (; at + (U - 1) * step + N <= c1; at += U * step) {
         Batch<T> v;
         load_batch<T, Threads, Nt>(v, z, at);
         add_batch<T>(a, v, c);
+        if constexpr (Keep) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                stash[slot + u * Threads] = __builtin_bit_cast(Stash<T>, (Packed<T>)v[u]);
+            slot += U * Threads;
+        }
     }
     for (; at < c1; at += step) {
         const int64_t left = (int64_t)(c1 - at);
-        fvec<N> f[1] = {to_f32<T, N>(load_vec<T, N>(z + at, left))};
+        const vec<T, N> v = load_vec<T, N>(z + at, left);
+        if constexpr (Keep) {
+            stash[slot] = __builtin_bit_cast(Stash<T>, (Packed<T>)v);
+            slot += Threads;
+        }
+        fvec<N> f[1] = {to_f32<T, N>(v)};
 #pragma unroll
         for (int j = 0; j < N; ++j)
             f[0][j] = j < left ? f[0][j] : -__builtin_inff();
@@ -144,21 +177,37 @@ __device__ __forceinline__ void add_row(Sum &a, const T *z, uint64_t c0, uint64_
     }
 }
 
-// dz = value(z) over columns [c0, c1).
-template <typename T, int Threads, bool Nt, typename F>
-__device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t c1, F value)
+// dz = value(z) over columns [c0, c1), with Kept from the stash.
+template <typename T, int Threads, bool Nt, bool Kept = false, typename F>
+__device__ __forceinline__ void map_row(const T *z, T *dz, uint64_t c0, uint64_t c1, F value,
+                                        const Stash<T> *stash = nullptr)
 {
     constexpr int N = kVec<T>, U = kFlight;
     constexpr uint64_t step = (uint64_t)Threads * N;
     uint64_t at = c0 + (uint64_t)threadIdx.x * N;
+    uint32_t slot = threadIdx.x;
     for (; at + (U - 1) * step + N <= c1; at += U * step) {
         Batch<T> v;
-        load_batch<T, Threads, Nt>(v, z, at);
+        if constexpr (Kept) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                v[u] = __builtin_bit_cast(Packed<T>, stash[slot + u * Threads]);
+            slot += U * Threads;
+        } else {
+            load_batch<T, Threads, Nt>(v, z, at);
+        }
         put_batch<T, Threads>(dz, v, at, value);
     }
     for (; at < c1; at += step) {
         const int64_t left = (int64_t)(c1 - at);
-        fvec<N> f = to_f32<T, N>(load_vec<T, N>(z + at, left));
+        vec<T, N> v;
+        if constexpr (Kept) {
+            v = __builtin_bit_cast(Packed<T>, stash[slot]);
+            slot += Threads;
+        } else {
+            v = load_vec<T, N>(z + at, left);
+        }
+        fvec<N> f = to_f32<T, N>(v);
 #pragma unroll
         for (int j = 0; j < N; ++j)
             f[j] = value(f[j]);
@@ -313,14 +362,17 @@ __device__ __forceinline__ float reduce_get(const float *part)
 // loads travel while the row is summed.  Both passes together read the row
 // twice and write it once, and all of that goes through the fabric between
 // the compute units and the last cache, which bounds the call (3 GB at 7 TB/s
-// for 4096 x 131072 bf16; without the exponentials it took as long).  So the
-// row's first `kept` batches stay in LDS, each thread's own vectors: 423 ->
-// 393 us there, 8192 x 65536 395 -> 368.
-template <typename T, int Threads, bool Grad, bool Nt>
-__global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uint32_t kept)
+// for 4096 x 131072 bf16; without the exponentials it took as long).  So each
+// thread keeps its own vectors of the row's first columns between the passes:
+// Held batches in registers (two workgroups of 512 then fill a compute unit),
+// those up to column `kept` in LDS.  LDS alone brought 423 -> 393 us there,
+// registers no more (5.6 TB/s of what has to move; a plain copy of that size
+// reaches 5.4), but 8192 x 50021 388 -> 347 and 2048 x 131072 float32 435 ->
+// 415; 8192 x 8000, all of it in LDS, 65 -> 56.
+template <typename T, int Threads, int Held, bool Grad, bool Nt>
+__global__ __launch_bounds__(Threads, Held ? 4 : 8) void distill_loss_kernel(Distill a,
+                                                                             uint64_t kept)
 {
-    using Stash = uint32_t __attribute__((ext_vector_type(4)));
-    using Packed = T __attribute__((ext_vector_type(kVec<T>)));
     constexpr int Waves = Threads / kWave;
     constexpr uint64_t width = (uint64_t)Threads * kVec<T> * kFlight;
     const uint64_t first = threadIdx.x * kVec<T>;
@@ -347,19 +399,21 @@ __global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uin
     e.own = load_entry<T>(a, row, tid);
     const float c = kLog2e / a.temp;
     Sum r = {kLowest, 0.0f};
-    Stash *stash = (Stash *)((char *)lds + entry_bytes(a.k));   // [batches][kFlight][Threads]
-    for (uint32_t b = 0; b < kept; ++b) {
-        Batch<T> v;
-        load_batch<T, Threads, true>(v, z, first + b * width);
-        add_batch<T>(r, v, c);
+    Stash<T> *stash = (Stash<T> *)((char *)lds + entry_bytes(a.k));   // [slots][Threads]
+    Batch<T> held[Held ? Held : 1];
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u)
-            stash[(b * kFlight + u) * Threads + tid] = __builtin_bit_cast(Stash, (Packed)v[u]);
-    }
+    for (int b = 0; b < Held; ++b)
+        load_batch<T, Threads, true>(held[b], z, first + b * width);
+#pragma unroll
+    for (int b = 0; b < Held; ++b)
+        add_batch<T>(r, held[b], c);
+    if constexpr (Grad)
+        add_row<T, Threads, true, true>(r, z, Held * width, kept, c, stash);
     // the entries' columns have arrived by the row's middle
     constexpr uint64_t step = width / kFlight;
-    const uint64_t half = a.vocab / (2 * step) * step, mid = kept ? kept * width : half;
-    add_row<T, Threads, Nt>(r, z, kept * width, mid, c);
+    const uint64_t mid = kept ? kept : a.vocab / (2 * step) * step;
+    if (!kept)
+        add_row<T, Threads, Nt>(r, z, 0, mid, c);
     e.read_logits(a, row, z, 0, a.vocab);
     add_row<T, Threads, Nt>(r, z, mid, a.vocab, c);
     r = join_lanes<kWave>(r, c);
@@ -396,14 +450,13 @@ __global__ __launch_bounds__(Threads, 8) void distill_loss_kernel(Distill a, uin
         }
         const float g = s / a.temp, inv = 1.0f / r.s, f = g / r.s;
         const auto value = [=](float x) { return exp2_hw((x - r.m) * c) * f; };
-        for (uint32_t b = 0; b < kept; ++b) {
-            Batch<T> v;
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u)
-                v[u] = __builtin_bit_cast(Packed, stash[(b * kFlight + u) * Threads + tid]);
-            put_batch<T, Threads>(dz, v, first + b * width, value);
+        for (int b = 0; b < Held; ++b) {
+            hide<T>(held[b]);
+            put_batch<T, Threads>(dz, held[b], first + b * width, value);
         }
-        map_row<T, Threads, true>(z, dz, kept * width, a.vocab, value);
+        map_row<T, Threads, true, true>(z, dz, Held * width, kept, value, stash);
+        map_row<T, Threads, true>(z, dz, kept, a.vocab, value);
         __syncthreads();
         e.put(a, dz, 0, a.vocab, g, w[0],
               [=](float x) { return exp2_hw((x - r.m) * c) * inv; });
@@ -462,22 +515,26 @@ __global__ __launch_bounds__(Threads) void distill_grad_kernel(Distill a, uint64
 template <typename T, int Threads>
 void loss(const Distill &a, hipStream_t s)
 {
+    const auto kernel = a.rows * a.vocab * sizeof(T) >= kStreamBytes
+                            ? distill_loss_kernel<T, Threads, 0, false, true>
+                            : distill_loss_kernel<T, Threads, 0, false, false>;
+    kernel<<<block_grid(a.rows), Threads, entry_bytes(a.k), s>>>(a, 0);
+}
+
+// Rows of at least Held batches.
+template <typename T, int Threads, int Held>
+void loss_grad(const Distill &a, hipStream_t s)
+{
+    // vectors a thread that fit the workgroup's share of a compute unit's LDS
+    constexpr uint64_t step = (uint64_t)Threads * kVec<T>, held = Held * kFlight * step;
+    constexpr uint32_t waves = Held ? 16 : 32, slot = Threads * 16;
+    constexpr uint32_t share = dev::kLdsBytesPerCu / (waves * kWave / Threads) - 512u;
     const uint32_t lds = entry_bytes(a.k);
-    if (a.dz) {
-        // batches that fit the workgroup's share of a compute unit's LDS
-        const uint32_t batch = Threads * 16 * kFlight;
-        const uint32_t share = dev::kLdsBytesPerCu / (2048 / Threads) - 512u;
-        const uint64_t all = a.vocab * sizeof(T) / batch;
-        uint32_t kept = lds < share ? (share - lds) / batch : 0;
-        kept = all < kept ? (uint32_t)all : kept;
-        distill_loss_kernel<T, Threads, true, false>
-            <<<block_grid(a.rows), Threads, lds + kept * batch, s>>>(a, kept);
-    } else {
-        const auto kernel = a.rows * a.vocab * sizeof(T) >= kStreamBytes
-                                ? distill_loss_kernel<T, Threads, false, true>
-                                : distill_loss_kernel<T, Threads, false, false>;
-        kernel<<<block_grid(a.rows), Threads, lds, s>>>(a, 0);
-    }
+    const uint64_t room = held + (lds < share ? (share - lds) / slot : 0) * step;
+    const uint64_t kept = a.vocab < room ? a.vocab : room;
+    const uint32_t slots = (uint32_t)((kept - held + step - 1) / step);
+    distill_loss_kernel<T, Threads, Held, true, false>
+        <<<block_grid(a.rows), Threads, lds + slots * slot, s>>>(a, kept);
 }
 
 template <typename T>
@@ -486,18 +543,25 @@ hipError_t loss(const Distill &a, hipStream_t s)
     // A workgroup for a few vectors a lane.  Long rows get few, large
     // workgroups: with many rows in flight at once they no longer stay in the
     // caches between the two passes.  Loss and gradient in bf16, us with 64 /
-    // 256 / 512 / 1024 threads: 8192 x 1000 19 / 32 / 57 / 146; 8192 x 8000 83
-    // / 75 / 90 / 169; 8192 x 32000 300 / 242 / 224 / 278; 4096 x 131072 633 /
-    // 579 / 486 / 437.
+    // 256 / 512 / 1024 threads and nothing held: 8192 x 1000 19 / 32 / 57 /
+    // 146; 8192 x 8000 83 / 75 / 90 / 169; 8192 x 32000 300 / 242 / 224 / 278;
+    // 4096 x 131072 633 / 579 / 486 / 437.  Batches held in registers: 8192 x
+    // 16000 99 with one, 107 without; 8192 x 40000 249 with two, 244 without;
+    // 8192 x 50021 347 with three, 388 without; 4096 x 100000 303 with four,
+    // 311 with three.
     const uint64_t bytes = a.vocab * sizeof(T);
     if (bytes <= 8192)
-        loss<T, 64>(a, s);
+        a.dz ? loss_grad<T, 64, 0>(a, s) : loss<T, 64>(a, s);
     else if (bytes <= 32768)
-        loss<T, 256>(a, s);
+        !a.dz             ? loss<T, 256>(a, s)
+        : bytes >= 16384  ? loss_grad<T, 256, 1>(a, s)
+                          : loss_grad<T, 256, 0>(a, s);
     else if (bytes <= 98304)
-        loss<T, 512>(a, s);
+        a.dz ? loss_grad<T, 512, 0>(a, s) : loss<T, 512>(a, s);
     else
-        loss<T, 1024>(a, s);
+        !a.dz             ? loss<T, 1024>(a, s)
+        : bytes >= 131072 ? loss_grad<T, 512, 4>(a, s)
+                          : loss_grad<T, 512, 3>(a, s);
     return hipGetLastError();
 }
 

@@ -127,6 +127,27 @@ def test_many_rows(gpu, kind):
     check(gpu.distill_loss_grad(z, idx, top, 1.5, rs, 3.0), want, V, kind)
 
 
+@pytest.mark.parametrize("kind", TYPES)
+def test_row_lengths(gpu, kind):
+    """Rows around the lengths at which more or less of a row is kept between
+    the two passes, and other numbers of entries beside it."""
+    import torch
+
+    size = torch.finfo(dtype(kind)).bits // 8
+    for nbytes, k in ((8192, 1), (8192, 1024), (16384, 40), (18432, 1024), (32768, 5), (40000, 300),
+                      (65536, 1024), (73728, 8), (98304, 64), (114688, 1024), (131072, 1),
+                      (204800, 40), (212992, 1024)):
+        for V in (nbytes // size - 1, nbytes // size, nbytes // size + 1):
+            print("[gpu] distill", kind, V, k, flush=True)
+            z, idx, top, rs = case(V, 3, V, k, kind, extra=V % 3)
+            want = plain(z, idx, top, 1.5, rs, 2.0)
+            wide = torch.full((3, V + 3), 7.0, dtype=dtype(kind), device="cuda")
+            got = gpu.distill_loss_grad(z, idx, top, 1.5, rs, 2.0, out=wide[:, :V])
+            check(got, want, V, kind)
+            assert (wide[:, V:] == 7.0).all()
+            assert torch.equal(gpu.distill_loss_grad(z, idx, top, 1.5, rs, 2.0, out=z)[2], got[2])
+
+
 def test_rows_with_nothing(gpu):
     """No entry, entries of -inf alone, masked rows, logits of -inf or of the
     type's lowest value, and rows that hold NaN but are not read."""
