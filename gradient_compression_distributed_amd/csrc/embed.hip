@@ -563,14 +563,15 @@ __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64
 // finished here; one that reaches over an end leaves its sum in part[run][0]
 // (it began before the run) or part[run][1].  kWrite: the workgroups behind
 // the first `blocks` zero the rows that no position names, in pieces of 64 KiB
-// (50021 x 1001 float32, all in all: 62 us; 16 KiB 64.5, 256 KiB 62).
+// (4001 positions into 50021 x 1001 float32, sorting and all: 62 us, 16 KiB
+// 64.5, 256 KiB 62, before ordinary accesses below 32 MiB made it 56).
 //
-// Bound by memory: 65536 x 2048 bf16 into 20000 rows moves 445 MB in 87 us (5.1
-// TB/s), 16384 x 4096 bf16 added to a 2 GiB table 366 MB in 76 us (4.8 TB/s,
-// reads and writes of scattered rows); a copy of that size reaches 5.4.
+// Bound by memory: 65536 x 2048 bf16 into 20000 rows moves 442 MB in 88 us (5.0
+// TB/s), 16384 x 4096 bf16 added to a 2 GiB table 364 MB in 67 us (5.4 TB/s);
+// a copy of that size reaches 5.4.
 // Prefetching the next batch, other batches and longer or shorter runs changed
 // nothing.  Nt: the gradient is read and the sums stored non-temporally, from
-// 32 MiB of gradient on (the last case: 102 us, with ordinary accesses 110; but
+// 32 MiB of gradient on (the last case, all in all: 102 us, with ordinary accesses 110; but
 // 4001 x 1001 float32 61 against 58.5, as smaller ones are still in the caches).
 template <typename T, Form F, bool Nt>
 __global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t cols,
