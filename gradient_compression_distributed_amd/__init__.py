@@ -561,12 +561,12 @@ def qsgd_elias_decode(words, offsets, n: int, d: int, norms=None, nibbles=None):
 # its tensors, on that device's current stream, whatever device is current.
 # What a call needs of torch, looked up once (by _lm): the small calls take a
 # few microseconds, and an import statement or a Stream object is a part of it.
-_torch = _type_codes = _raw_stream = _current_device = None
+_torch = _tensor = _type_codes = _raw_stream = _current_device = None
 
 
 def _lm():
     """The library, with the names above set."""
-    global _torch, _type_codes, _raw_stream, _current_device
+    global _torch, _tensor, _type_codes, _raw_stream, _current_device
     if _torch is None:
         import torch
 
@@ -576,7 +576,7 @@ def _lm():
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-        _torch = torch
+        _torch, _tensor = torch, torch.Tensor
     return _lib if _lib is not None else load()
 
 
@@ -602,33 +602,53 @@ def _on(x, name, device=None):
     return at
 
 
-def _matrix(x, name, rows, cols, device, written=False):
-    """Checks a matrix of rows x cols (at least ``rows`` rows if it is
-    written); returns the distance of its rows in elements."""
-    _on(x, name, device)
-    shape = x.shape
-    if len(shape) != 2 or shape[1] != cols or (shape[0] < rows if written else shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(shape)}, needs ({rows}, {cols})")
+def _row_distance(x, name, rows, cols):
+    """The distance of a matrix's rows in elements."""
     ld, step = x.stride()
-    if cols > 1 and step != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if shape[0] <= 1:
+    if rows <= 1:
         return cols
     if ld < cols:
         raise ValueError(f"{name}: rows overlap")
     return ld
 
 
+def _first(x, name):
+    """A call's first matrix: (index of the device, rows, columns, distance of
+    the rows)."""
+    dev = _on(x, name)
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be a matrix")
+    rows, cols = shape
+    return dev, rows, cols, _row_distance(x, name, rows, cols)
+
+
+def _matrix(x, name, rows, cols, device, written=False):
+    """Checks a matrix of rows x cols (at least ``rows`` rows if it is
+    written); returns the distance of its rows in elements."""
+    if type(x) is not _tensor or x.get_device() != device:
+        _on(x, name, device)
+    shape = x.shape
+    if shape != (rows, cols) and (len(shape) != 2 or shape[1] != cols or not written or shape[0] < rows):
+        raise ValueError(f"{name} has shape {tuple(shape)}, needs ({rows}, {cols})")
+    return _row_distance(x, name, shape[0], cols)
+
+
 def _vector(x, name, n, device, dtype=None, at_least=False):
-    """Checks a contiguous tensor of n elements (or at least n)."""
-    _on(x, name, device)
+    """Checks a contiguous tensor of n elements (or at least n, or any number
+    for None); returns how many it holds."""
+    if type(x) is not _tensor or x.get_device() != device:
+        _on(x, name, device)
     if dtype is not None and x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {x.dtype})")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     have = x.numel()
-    if have < n if at_least else have != n:
+    if have != n and n is not None and (have < n or not at_least):
         raise ValueError(f"{name} holds {have} elements, needs {n}")
+    return have
 
 
 def _call(fn, where, device, *args):
@@ -655,14 +675,8 @@ def embed_lookup(table, tokens, scale: float = 1.0, out=None):
     """out[i] = scale * table[tokens[i]], rounded once to out's type (the
     table's by default).  Tokens outside the table are padding: zero rows."""
     lib, torch = _lm(), _torch
-    dev = _on(table, "table")
-    if table.dim() != 2:
-        raise ValueError("table must be a matrix")
-    vocab, dim = table.shape
-    ld = _matrix(table, "table", vocab, dim, dev)
-    _on(tokens, "tokens", dev)
-    n = tokens.numel()
-    _vector(tokens, "tokens", n, dev)
+    dev, vocab, dim, ld = _first(table, "table")
+    n = _vector(tokens, "tokens", None, dev)
     if out is None:
         out = torch.empty((n, dim), dtype=table.dtype, device=table.device)
     out_ld = _matrix(out, "out", n, dim, dev)
@@ -685,8 +699,7 @@ def embed_sort(tokens, vocab: int, plan=None) -> EmbedPlan:
     plan of as many tokens is overwritten if given."""
     lib, torch = _lm(), _torch
     dev = _on(tokens, "tokens")
-    n = tokens.numel()
-    _vector(tokens, "tokens", n, dev)
+    n = _vector(tokens, "tokens", None, dev)
     if plan is None:
         plan = EmbedPlan(torch.empty(lib.embed_plan_words(n), dtype=torch.int32,
                                      device=tokens.device), n, vocab)
@@ -703,13 +716,11 @@ def _embed_grad_args(lib, grad, plan, work):
     """The checks embed_grad and embed_grad_rows share; (device, row length,
     distance of the gradient's rows, workspace)."""
     torch = _torch
-    dev = _on(grad, "grad")
+    dev, rows, dim, ld = _first(grad, "grad")
     if not isinstance(plan, EmbedPlan):
         raise TypeError("plan must be an EmbedPlan (embed_sort)")
-    if grad.dim() != 2:
-        raise ValueError("grad must be a matrix")
-    dim = grad.shape[1]
-    ld = _matrix(grad, "grad", plan.n, dim, dev)
+    if rows != plan.n:
+        raise ValueError(f"grad has {rows} rows, the plan {plan.n} tokens")
     _vector(plan.words, "plan", lib.embed_plan_words(plan.n), dev, torch.int32, at_least=True)
     need = lib.embed_work_bytes(plan.n, dim)
     if work is None:
@@ -772,20 +783,21 @@ def _rms_args(x, weight, residual, h, rstd):
     arguments of x and the residual, arguments of the weight, h, its
     arguments, rstd)."""
     torch = _torch
-    dev = _on(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix")
-    rows, dim = x.shape
+    dev, rows, dim, ld = _first(x, "x")
     kind = _type_code(x, "x")
     res, res_ld, h_at, h_ld = None, 0, None, 0
-    ld = _matrix(x, "x", rows, dim, dev)
     if residual is not None:
+        res_ld = _matrix(residual, "residual", rows, dim, dev)
         _type_code(residual, "residual", (kind,))
-        res, res_ld = residual.data_ptr(), _matrix(residual, "residual", rows, dim, dev)
-        if h is None:
-            h = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
-        _type_code(h, "h", (kind,))
-        h_at, h_ld = h.data_ptr(), _matrix(h, "h", rows, dim, dev)
+        res = residual.data_ptr()
+        if h is residual:
+            h_at, h_ld = res, res_ld
+        else:
+            if h is None:
+                h = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
+            h_ld = _matrix(h, "h", rows, dim, dev)
+            _type_code(h, "h", (kind,))
+            h_at = h.data_ptr()
     elif h is not None:
         raise ValueError("h is x itself without a residual")
     _vector(weight, "weight", dim, dev)
@@ -843,12 +855,8 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, accumulat
     residual; it may be given as dh.  dweight is float32; with ``accumulate``
     it is added to."""
     lib, torch = _lm(), _torch
-    dev = _on(dy, "dy")
-    if dy.dim() != 2:
-        raise ValueError("dy must be a matrix")
-    rows, dim = dy.shape
+    dev, rows, dim, ld = _first(dy, "dy")
     kind = _type_code(dy, "dy")
-    ld = _matrix(dy, "dy", rows, dim, dev)
     h_ld = _matrix(h, "h", rows, dim, dev)
     _type_code(h, "h", (kind,))
     _vector(weight, "weight", dim, dev)
@@ -880,12 +888,8 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, accumulat
 def _distill_args(logits, index, teacher, temperature, row_scale, scale):
     """The checks the three calls share; (device, rows, vocab, type, the
     logits' arguments, the arguments behind them)."""
-    dev = _on(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be a matrix")
-    rows, vocab = logits.shape
+    dev, rows, vocab, ld = _first(logits, "logits")
     kind = _type_code(logits, "logits")
-    ld = _matrix(logits, "logits", rows, vocab, dev)
     _on(index, "index", dev)
     k = index.shape[-1] if index.dim() else 0
     idx_ld = _matrix(index, "index", rows, k, dev)
