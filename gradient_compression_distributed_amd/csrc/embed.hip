@@ -458,90 +458,23 @@ __device__ __forceinline__ uint32_t starts_before(const EmbedGrad &e, uint64_t t
     return sum_counts(lane < tile ? e.tiles[lane] : 0u);
 }
 
-// p[0..count) = 0 by 256 threads, in aligned vectors but for the ends.
-__device__ __forceinline__ void zero_floats(float *p, uint64_t count)
+// Zeroes the dense gradient's `rows` rows of `dim` before the sums are written
+// over those that are named (one row of all when they lie side by side): a
+// workgroup per 4 KiB, one store a lane.  That order of stores reaches 6.85
+// TB/s (1 GiB in 157 us), where workgroups of 16 or 64 KiB take 175 or 197 us
+// and workgroups that stride through the table 194 to 270.  Zeroing the
+// other rows alone, by workgroups behind the sums' own, took 207 us against 175
+// for 1000 positions into 65536 x 4096, 52 against 48 for 4001 into 50021 x
+// 1001, 23 against 13 for 2000 into 8000 x 512 (each store waited for a search
+// of the keys), and 119 against 127 for 65536 into 32000 x 2048.
+__global__ __launch_bounds__(256) void embed_zero_kernel(float *out, uint64_t rows, uint64_t dim,
+                                                         uint64_t ld, uint64_t vectors)
 {
-    GCQ_G float *q = (GCQ_G float *)p;
-    const uint32_t tid = threadIdx.x;
-    const uint64_t skip = (4u - ((uintptr_t)p / 4u) % 4u) % 4u, head = skip < count ? skip : count;
-    if (tid < head)
-        q[tid] = 0.0f;
-    const uint64_t body = (count - head) / 4u;
-    const dev::v4f zero = 0.0f;
-    for (uint64_t i = tid; i < body; i += 256u)
-        ((GCQ_G dev::v4f *)(q + head))[i] = zero;
-    const uint64_t at = head + 4u * body + tid;
-    if (at < count)
-        q[at] = 0.0f;
-}
-
-// Zeroes the rows [v0, v0 + span) of the dense gradient that no position
-// names, span <= 64.  128 threads each search for the first position of a row
-// >= v0 and of one >= v0 + span, a 128th of the range at a time; the
-// positions between name the rows to leave.
-__device__ __forceinline__ void zero_rows(const EmbedGrad &e, uint64_t v0, uint32_t span)
-{
-    __shared__ uint32_t votes[4];
-    __shared__ unsigned long long named;
-    const uint32_t tid = threadIdx.x, side = tid / 128u;
-    const uint64_t target = v0 + (side ? span : 0u);
-    uint64_t lo[2] = {0, 0}, hi[2] = {e.n, e.n};
-    if (tid == 0)
-        named = 0;
-    while (lo[0] < hi[0] || lo[1] < hi[1]) {
-        const uint64_t step = (hi[side] - lo[side] + 127u) / 128u;
-        const uint64_t at = lo[side] + (tid % 128u) * step;
-        const uint64_t m = __ballot(at < hi[side] && e.keys[at] < target);
-        if ((tid & (kWave - 1)) == 0)
-            votes[tid / kWave] = (uint32_t)__popcll(m);
-        __syncthreads();
-#pragma unroll
-        for (uint32_t s = 0; s < 2; ++s) {
-            const uint32_t below = votes[2 * s] + votes[2 * s + 1];   // probes below the target
-            const uint64_t st = (hi[s] - lo[s] + 127u) / 128u;
-            const uint64_t end = lo[s] + below * st;
-            hi[s] = end < hi[s] ? end : hi[s];
-            lo[s] = below ? lo[s] + (below - 1u) * st + 1u : lo[s];
-            if (!below)
-                hi[s] = lo[s];
-        }
-        __syncthreads();
-    }
-    __syncthreads();   // named is 0
-    const uint64_t a = lo[0], b = lo[1];
-    if (b - a <= 1024u) {
-        uint64_t mine = 0;
-        for (uint64_t i = a + tid; i < b; i += 256u)
-            mine |= 1ull << (e.keys[i] - v0);
-        if (mine)
-            atomicOr(&named, (unsigned long long)mine);
-    } else if (tid < kWave) {   // long segments: each row looks for its first position
-        uint64_t l = a, h = b;
-        while (l < h) {
-            const uint64_t mid = (l + h) / 2;
-            if (e.keys[mid] < v0 + tid)
-                l = mid + 1;
-            else
-                h = mid;
-        }
-        const uint64_t m = __ballot(l < b && e.keys[l] == v0 + tid);
-        if (tid == 0)
-            named = m;
-    }
-    __syncthreads();
-    const uint64_t rows = e.vocab - v0 < span ? e.vocab - v0 : span;
-    uint64_t m = ~(uint64_t)named;
-    if (rows < 64)
-        m &= (1ull << rows) - 1u;
-    // neighbouring rows without a gap are one stretch
-    const bool dense = e.out_ld == e.dim;
-    while (m) {
-        const uint32_t r = (uint32_t)__builtin_ctzll(m);
-        const uint64_t rest = ~(m >> r);
-        const uint32_t count = !dense ? 1u : rest ? (uint32_t)__builtin_ctzll(rest) : 64u - r;
-        zero_floats(e.out + (v0 + r) * e.out_ld, count * e.dim);
-        m &= count + r >= 64 ? 0ull : ~0ull << (r + count);
-    }
+    const uint64_t i = block_number() * 256u + threadIdx.x;   // `vectors` to a row
+    const uint64_t row = rows == 1 ? 0 : i / vectors, c = (i - row * vectors) * 4u;
+    const vec<float, 4> zero = 0.0f;
+    if (row < rows && c < dim)
+        store_vec<float, 4>(out + row * ld + c, zero, (int64_t)(dim - c));
 }
 
 // Where a finished sum goes; `old` is what is there (kAdd).
@@ -561,36 +494,24 @@ __device__ __forceinline__ void put_row(const EmbedGrad &e, uint64_t row, uint64
 // longer).  Keys and positions are the wavefront's own, so they are scalar
 // loads and every branch on them is uniform.  A segment inside the run is
 // finished here; one that reaches over an end leaves its sum in part[run][0]
-// (it began before the run) or part[run][1].  kWrite: the workgroups behind
-// the first `blocks` zero the rows that no position names, in pieces of 64 KiB
-// (4001 positions into 50021 x 1001 float32, sorting and all: 62 us, 16 KiB
-// 64.5, 256 KiB 62, before ordinary accesses below 32 MiB made it 56).
+// (it began before the run) or part[run][1].
 //
 // Bound by memory: 65536 x 2048 bf16 into 20000 rows moves 442 MB in 88 us (5.0
 // TB/s), 16384 x 4096 bf16 added to a 2 GiB table 364 MB in 67 us (5.4 TB/s);
 // a copy of that size reaches 5.4.
 // Prefetching the next batch, other batches and longer or shorter runs changed
 // nothing.  Nt: the gradient is read and the sums stored non-temporally, from
-// 32 MiB of gradient on (the last case, all in all: 102 us, with ordinary accesses 110; but
-// 4001 x 1001 float32 61 against 58.5, as smaller ones are still in the caches).
+// 32 MiB of gradient on (the last case, all in all: 102 us, with ordinary
+// accesses 110; but 4001 x 1001 float32 into 50021 rows 61 against 58.5, as
+// smaller gradients are still in the caches).
 template <typename T, Form F, bool Nt>
-__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t cols,
-                                                         uint64_t blocks, uint32_t span)
+__global__ __launch_bounds__(256) void embed_grad_kernel(EmbedGrad e, uint32_t cols)
 {
     using Scalar = const __attribute__((address_space(4))) uint32_t;
     constexpr int N = 4, U = F == Form::kAdd ? 4 : 8;
-    const uint64_t block = block_number();
-    if constexpr (F == Form::kWrite) {
-        if (block >= blocks) {
-            const uint64_t v0 = (block - blocks) * span;
-            if (v0 < e.vocab)
-                zero_rows(e, v0, span);
-            return;
-        }
-    }
     const uint32_t lane = threadIdx.x & (kWave - 1);
     const uint64_t item =
-        block * 4u + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+        block_number() * 4u + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
     const uint64_t run = item / cols, n = e.n, i0 = run * e.run;
     const uint64_t c = (item % cols * kWave + lane) * N;
     if (i0 >= n)
@@ -882,15 +803,11 @@ template <typename T, Form F>
 void sum_runs(const EmbedGrad &e, uint64_t runs, hipStream_t s)
 {
     const uint32_t cols = (uint32_t)((e.dim + 255) / 256);
-    const uint64_t blocks = (runs * cols + 3) / 4;
-    // rows that a zeroing workgroup looks at: about 64 KiB, 64 at most
-    const uint32_t span = (uint32_t)(e.dim >= 16384 ? 1u : e.dim <= 256 ? 64u : 16384 / e.dim);
-    const uint64_t zero = F == Form::kWrite ? (e.vocab + span - 1) / span : 0;
-    const dim3 grid = block_grid(blocks + zero);
+    const dim3 grid = block_grid((runs * cols + 3) / 4);
     if (e.n * e.dim * sizeof(T) >= (32ull << 20))
-        embed_grad_kernel<T, F, true><<<grid, 256, 0, s>>>(e, cols, blocks, span);
+        embed_grad_kernel<T, F, true><<<grid, 256, 0, s>>>(e, cols);
     else
-        embed_grad_kernel<T, F, false><<<grid, 256, 0, s>>>(e, cols, blocks, span);
+        embed_grad_kernel<T, F, false><<<grid, 256, 0, s>>>(e, cols);
 }
 
 template <Form F>
@@ -911,9 +828,15 @@ hipError_t grad(EmbedGrad e, hipStream_t s)
                 embed_scan_kernel<<<1, kScanThreads, 0, s>>>(runs ? e.tiles : (uint32_t *)e.count,
                                                              tiles, runs ? e.count : nullptr);
         }
-        if (!runs)
-            return hipGetLastError();
     }
+    if constexpr (F == Form::kWrite) {
+        const uint64_t rows = e.out_ld == e.dim ? 1 : e.vocab;
+        const uint64_t dim = rows == 1 ? e.vocab * e.dim : e.dim, vectors = (dim + 3) / 4;
+        embed_zero_kernel<<<block_grid((rows * vectors + 255) / 256), 256, 0, s>>>(
+            e.out, rows, dim, e.out_ld, vectors);
+    }
+    if (!runs)
+        return hipGetLastError();
     switch (e.type) {
     case GCQ_F32: sum_runs<float, F>(e, runs, s); break;
     case GCQ_F16: sum_runs<_Float16, F>(e, runs, s); break;
