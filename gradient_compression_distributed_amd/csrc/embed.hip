@@ -21,13 +21,16 @@ using namespace lm;
 
 // ------------------------------------------------------------------ lookup
 // L lanes share a row (a power of two up to 256), so a workgroup of 256
-// threads copies 256 / L rows at once, R times over.  The R tokens are loaded
-// together and then the R rows' vectors, so a row waits for one load, not for
-// two in turn (32768 rows of 4096 bf16, us for R = 1 / 2 / 4 / 8: 80 / 75 / 82 /
-// 83).  Bound by the fabric: rows of frequent tokens come from the last cache,
+// threads copies 256 / L rows at once, R times over, and of each at most
+// kLookupTrips vectors a lane: `cols` workgroups share a longer row (16000 rows
+// of 8192 float32 131 us, by one workgroup each 145; with one vector a lane
+// 136).  The R tokens are loaded together and then the R rows' vectors, so a
+// row waits for one load, not for two in turn (32768 rows of 4096 bf16, us for
+// R = 1 / 2 / 4 / 8: 80 / 75 / 82 / 83).  Bound by the fabric: rows of frequent tokens come from the last cache,
 // 268 MB out and as much in at 7.2 TB/s.  A few rows take a launch (3 us).
 template <typename T, typename O>
 constexpr int kLookup = kVec<T> < kVec<O> ? kVec<T> : kVec<O>;   // 16 bytes at most on either side
+constexpr uint32_t kLookupTrips = 2;
 
 template <typename T, typename O, typename I, int R>
 __global__ __launch_bounds__(256) void embed_lookup_kernel(const T *__restrict__ table,
@@ -36,18 +39,21 @@ __global__ __launch_bounds__(256) void embed_lookup_kernel(const T *__restrict__
                                                            const I *__restrict__ tokens,
                                                            uint64_t n, float scale,
                                                            O *__restrict__ out, uint64_t out_ld,
-                                                           uint32_t lanes)
+                                                           uint32_t lanes, uint32_t cols)
 {
     constexpr int N = kLookup<T, O>;
     const uint32_t lane = threadIdx.x & (lanes - 1), slots = 256u / lanes;
-    const uint64_t row0 = block_number() * slots * R + threadIdx.x / lanes;   // then every slots-th
+    const uint64_t block = block_number();
+    const uint64_t row0 = block / cols * slots * R + threadIdx.x / lanes;   // then every slots-th
     uint64_t tok[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const uint64_t row = row0 + (uint64_t)r * slots;
         tok[r] = row < n ? (uint64_t)(int64_t)((const GCQ_G I *)tokens)[row] : ~0ull;
     }
-    for (uint64_t c = (uint64_t)lane * N; c < dim; c += (uint64_t)lanes * N) {
+    const uint64_t width = (uint64_t)lanes * N * kLookupTrips, c0 = block % cols * width;
+    const uint64_t c1 = c0 + width < dim ? c0 + width : dim;
+    for (uint64_t c = c0 + (uint64_t)lane * N; c < c1; c += (uint64_t)lanes * N) {
         const int64_t left = (int64_t)(dim - c);
         vec<T, N> v[R];
 #pragma unroll
@@ -710,10 +716,13 @@ hipError_t lookup(const EmbedTable &t, const void *tokens, uint64_t n, float sca
 {
     const uint32_t lanes = lanes_for(t.dim, kLookup<T, O>);
     const uint64_t per = 256u / lanes, blocks = (n + per - 1) / per;
-    const auto kernel = blocks >= 4096 ? embed_lookup_kernel<T, O, I, 2>
-                                       : embed_lookup_kernel<T, O, I, 1>;
-    kernel<<<block_grid(blocks >= 4096 ? (blocks + 1) / 2 : blocks), 256, 0, s>>>(
-        (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes);
+    const uint64_t width = (uint64_t)lanes * kLookup<T, O> * kLookupTrips;
+    const uint32_t cols = (uint32_t)((t.dim + width - 1) / width);
+    const bool two = blocks >= 4096;
+    const auto kernel = two ? embed_lookup_kernel<T, O, I, 2> : embed_lookup_kernel<T, O, I, 1>;
+    kernel<<<block_grid((two ? (blocks + 1) / 2 : blocks) * cols), 256, 0, s>>>(
+        (const T *)t.p, t.vocab, t.dim, t.ld, (const I *)tokens, n, scale, (O *)out, out_ld, lanes,
+        cols);
     return hipGetLastError();
 }
 
