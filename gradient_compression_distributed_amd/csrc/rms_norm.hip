@@ -405,67 +405,61 @@ struct Split {
 };
 
 template <typename T>
-Split split_row(uint64_t dim, uint64_t most)
+Split split_row(uint64_t dim, uint64_t most, bool half = false)   // half: 512 lanes, too
 {
     const uint64_t vecs = (dim + kVec<T> - 1) / kVec<T>;
-    for (int lanes : {64, 256}) {
+    for (int lanes : {64, 256, 512}) {
         const uint64_t ch = (vecs + lanes - 1) / lanes;
-        if (ch <= most)
+        if (ch <= most && (lanes < 512 || half))
             return {lanes, (int)ch};
     }
     return {1024, vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 && sizeof(T) == 4 ? 4 : 0};
 }
 
-template <typename T, int L, int Ch>
+template <typename T, int L, int Ch, bool Q8>
 void norm(const RmsNorm &a, hipStream_t s)
 {
     constexpr int threads = L < 256 ? 256 : L, per = threads / L;
-    const dim3 grid = block_grid((a.rows + per - 1) / per);
     // from 32 MiB a matrix the caches no longer hold them until their next use:
     // 8192 x 4096 bf16 47 us against 52, 2048 x 4096 (16 MiB) 14.3 against 14.1
-    const bool nt = a.rows * a.dim * sizeof(T) >= (32ull << 20);
-    if (a.codes) {
-        if (nt)
-            rms_norm_kernel<T, L, Ch, true, true><<<grid, threads, 0, s>>>(a);
-        else
-            rms_norm_kernel<T, L, Ch, true, false><<<grid, threads, 0, s>>>(a);
-    } else {
-        if (nt)
-            rms_norm_kernel<T, L, Ch, false, true><<<grid, threads, 0, s>>>(a);
-        else
-            rms_norm_kernel<T, L, Ch, false, false><<<grid, threads, 0, s>>>(a);
-    }
+    const auto kernel = a.rows * a.dim * sizeof(T) >= (32ull << 20)
+                            ? rms_norm_kernel<T, L, Ch, Q8, true>
+                            : rms_norm_kernel<T, L, Ch, Q8, false>;
+    kernel<<<block_grid((a.rows + per - 1) / per), threads, 0, s>>>(a);
 }
 
-template <typename T, int L>
+template <typename T, int L, bool Q8>
 void norm(const RmsNorm &a, int ch, hipStream_t s)
 {
     if (ch == 1)
-        norm<T, L, 1>(a, s);
+        norm<T, L, 1, Q8>(a, s);
     else if (ch == 2)
-        norm<T, L, 2>(a, s);
-    else if constexpr (L < 1024)
-        norm<T, L, 3>(a, s);
-    else if constexpr (sizeof(T) == 4)
-        norm<T, L, 4>(a, s);
+        norm<T, L, 2, Q8>(a, s);
+    else if constexpr (L < 1024 && !Q8)
+        norm<T, L, 3, Q8>(a, s);
+    else if constexpr (L == 1024 && sizeof(T) == 4)
+        norm<T, L, 4, Q8>(a, s);
 }
 
-template <typename T>
+// Many rows get up to three vectors a lane, to 8 bits two and 512 lanes before
+// 1024, us: to 8 bits 16000 x 5120 bf16 121 with two of 512 lanes, 153 with
+// three of 256; 8192 x 8192 81, one of 1024 lanes 86; plain, 112 and 112, 90
+// and 87; 2999 x 2051 float32 plain 10.4 with three of 256 lanes, 14.5 with one
+// of 1024.
+template <typename T, bool Q8>
 void norm(const RmsNorm &a, hipStream_t s)
 {
-    const Split p = split_row<T>(a.dim, a.rows >= 1024 ? 3 : 1);
-    if (!p.ch) {
-        if (a.codes)
-            rms_norm_long_kernel<T, true><<<block_grid(a.rows), 1024, 0, s>>>(a);
-        else
-            rms_norm_long_kernel<T, false><<<block_grid(a.rows), 1024, 0, s>>>(a);
-    } else if (p.lanes == 64) {
-        norm<T, 64>(a, p.ch, s);
-    } else if (p.lanes == 256) {
-        norm<T, 256>(a, p.ch, s);
-    } else {
-        norm<T, 1024>(a, p.ch, s);
-    }
+    const Split p = split_row<T>(a.dim, a.rows < 1024 ? 1 : Q8 ? 2 : 3, Q8);
+    if (!p.ch)
+        rms_norm_long_kernel<T, Q8><<<block_grid(a.rows), 1024, 0, s>>>(a);
+    else if (p.lanes == 64)
+        norm<T, 64, Q8>(a, p.ch, s);
+    else if (p.lanes == 256)
+        norm<T, 256, Q8>(a, p.ch, s);
+    else if (p.lanes == 1024)
+        norm<T, 1024, Q8>(a, p.ch, s);
+    else if constexpr (Q8)
+        norm<T, 512, Q8>(a, p.ch, s);
 }
 
 // Slots of the gradient: enough rows in flight to fill the device, few
@@ -533,9 +527,9 @@ uint64_t rms_norm_work_bytes(uint64_t rows, uint64_t dim, int type)
 hipError_t launch_rms_norm(const RmsNorm &a, hipStream_t stream)
 {
     switch (a.type) {
-    case GCQ_F32: norm<float>(a, stream); break;
-    case GCQ_F16: norm<_Float16>(a, stream); break;
-    default: norm<__bf16>(a, stream); break;
+    case GCQ_F32: a.codes ? norm<float, true>(a, stream) : norm<float, false>(a, stream); break;
+    case GCQ_F16: a.codes ? norm<_Float16, true>(a, stream) : norm<_Float16, false>(a, stream); break;
+    default: a.codes ? norm<__bf16, true>(a, stream) : norm<__bf16, false>(a, stream); break;
     }
     return hipGetLastError();
 }
