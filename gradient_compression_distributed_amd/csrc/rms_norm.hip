@@ -462,13 +462,28 @@ void norm(const RmsNorm &a, hipStream_t s)
         norm<T, 512, Q8>(a, p.ch, s);
 }
 
-// Slots of the gradient: enough rows in flight to fill the device, few
-// enough that their shares of dw are a small part of the traffic (16384 x 4096
-// bf16, us for 512 / 768 / 1024 / 1536 slots of 256 lanes: 109 / 101 / 101 /
-// 109; 8192 x 8192, 256 / 512 slots of 1024 lanes: 107 / 111).
-uint64_t grad_slots(uint64_t rows, int lanes)
+// The gradient's rows: two vectors a lane at most, 16-bit ones three of 256
+// lanes before 1024 (16000 x 5120 bf16 127 us against 141; but three of 64
+// lanes, 20000 x 1400, 73 against 55; 10000 x 2500 float32 three of 256 78, one
+// of 1024 76).
+template <typename T>
+Split grad_split(uint64_t dim)
 {
-    const uint64_t most = lanes == 64 ? 4096 : lanes == 256 ? 1024 : 256;
+    const Split p = split_row<T>(dim, 2);
+    return p.lanes == 1024 && sizeof(T) == 2 && dim <= 3 * 256 * kVec<T> ? Split{256, 3} : p;
+}
+
+// Slots of the gradient: what is resident at once, few enough that their shares
+// of dw are a small part of the traffic (16384 x 4096 bf16, us for 512 / 768 /
+// 1024 / 1536 slots of 256 lanes: 109 / 101 / 101 / 109; 16000 x 5120, three
+// vectors a lane, 768 / 1024: 127 / 156; 1024 lanes, 256 / 512 slots: 8192 x
+// 8192 bf16 107 / 111, 8192 x 4096 float32 99 / 94).
+template <typename T>
+uint64_t grad_slots(uint64_t rows, Split p)
+{
+    const uint64_t most = p.lanes == 64    ? 4096
+                          : p.lanes == 256 ? (p.ch == 3 ? 768 : 1024)
+                                           : (p.ch * kVec<T> == 4 ? 512 : 256);
     return rows < most ? rows : most;
 }
 
@@ -492,6 +507,8 @@ void norm_grad(const RmsGrad &a, int ch, hipStream_t s)
         norm_grad<T, L, 1>(a, s);
     else if (ch == 2)
         norm_grad<T, L, 2>(a, s);
+    else if constexpr (L == 256 && sizeof(T) == 2)
+        norm_grad<T, L, 3>(a, s);
     else if constexpr (L == 1024 && sizeof(T) == 4)
         norm_grad<T, L, 4>(a, s);
 }
@@ -499,8 +516,8 @@ void norm_grad(const RmsGrad &a, int ch, hipStream_t s)
 template <typename T>
 hipError_t norm_grad(RmsGrad a, hipStream_t s)
 {
-    const Split p = split_row<T>(a.dim, 2);
-    a.slots = grad_slots(a.rows, p.lanes);
+    const Split p = grad_split<T>(a.dim);
+    a.slots = grad_slots<T>(a.rows, p);
     if (a.rows) {
         if (!p.ch)
             rms_norm_grad_long_kernel<T><<<(uint32_t)a.slots, 1024, 0, s>>>(a);
@@ -520,8 +537,8 @@ hipError_t norm_grad(RmsGrad a, hipStream_t s)
 
 uint64_t rms_norm_work_bytes(uint64_t rows, uint64_t dim, int type)
 {
-    const Split p = type == GCQ_F32 ? split_row<float>(dim, 2) : split_row<_Float16>(dim, 2);
-    return 4 * dim * grad_slots(rows, p.lanes);
+    return 4 * dim * (type == GCQ_F32 ? grad_slots<float>(rows, grad_split<float>(dim))
+                                      : grad_slots<_Float16>(rows, grad_split<_Float16>(dim)));
 }
 
 hipError_t launch_rms_norm(const RmsNorm &a, hipStream_t stream)
