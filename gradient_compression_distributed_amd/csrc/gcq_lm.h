@@ -169,8 +169,8 @@ struct RmsGrad {
     void *dx;
     float *dw;
     bool add;                       // dw is added to
-    float *part_w;                  // workspace: [slots][dim]
-    uint64_t slots;
+    float *part_w;                  // workspace: [groups][dim]
+    uint64_t groups;                // workgroups
 };
 
 uint64_t rms_norm_work_bytes(uint64_t rows, uint64_t dim, int type);

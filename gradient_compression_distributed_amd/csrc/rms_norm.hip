@@ -32,7 +32,7 @@ constexpr float kMinNormal = 1.17549435e-38f;   // 2^-126: its reciprocal is fin
 template <int L, bool Max>
 __device__ __forceinline__ float row_reduce(float x, float *part)
 {
-    x = Max ? max_lanes(x) : sum_lanes(x);
+    x = Max ? max_lanes<L < kWave ? L : kWave>(x) : sum_lanes<L < kWave ? L : kWave>(x);
     if constexpr (L > kWave) {
         if ((threadIdx.x & (kWave - 1)) == 0)
             part[threadIdx.x / kWave] = x;
@@ -248,26 +248,25 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNorm a)
 }
 
 // ---------------------------------------------------------------- gradient
-// A slot is the L lanes that share a row; slot s takes rows s, s + slots, ...
-// and keeps its share of dw in registers, written to part_w[s] at the end, so
-// dy, h and dh are read once for both gradients.  Bound by memory: 16384 x 4096
+// L lanes share a row; slot s of them takes rows s, s + slots, ... and keeps its
+// share of dw in registers, so dy, h and dh are read once for both gradients.  A
+// workgroup adds its slots' shares at the end and writes them to part_w.  Bound by memory: 16384 x 4096
 // bf16 94 us of 100 (537 MB, 5.7 TB/s), the rest joins the shares.  Nt: the
 // matrices by non-temporal accesses.
 template <typename T, int L, int Ch, bool Nt>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_grad_kernel(RmsGrad a)
 {
     constexpr int N = kVec<T>, Threads = L < 256 ? 256 : L;
+    constexpr uint32_t Per = Threads / L;
     __shared__ float part[2][Threads / kWave];
     const uint32_t lane = threadIdx.x & (L - 1);
-    const uint64_t slot = (uint64_t)blockIdx.x * (Threads / L) + threadIdx.x / L;
-    if (slot >= a.slots)
-        return;   // only where a workgroup holds several slots: no barriers then
+    const uint64_t slot = (uint64_t)blockIdx.x * Per + threadIdx.x / L;
     fvec<N> dw[Ch];
 #pragma unroll
     for (int i = 0; i < Ch; ++i)
         dw[i] = 0.0f;
     uint32_t turn = 0;
-    for (uint64_t row = slot; row < a.rows; row += a.slots, turn ^= 1u) {
+    for (uint64_t row = slot; row < a.rows; row += a.groups * Per, turn ^= 1u) {
         const T *dy = (const T *)a.dy + row * a.dy_ld, *h = (const T *)a.h + row * a.h_ld;
         const T *dh = (const T *)a.dh + row * a.dh_ld;
         vec<T, N> gv[Ch], hv[Ch], dv[Ch];
@@ -315,15 +314,33 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_grad_kernel(RmsGra
             store_vec<T, N, Nt>((T *)a.dx + row * a.dx_ld + c, from_f32<T, N>(d), left);
         }
     }
+    float *pw = a.part_w + (uint64_t)blockIdx.x * a.dim;
+    if constexpr (Per == 1) {
 #pragma unroll
-    for (int i = 0; i < Ch; ++i) {
-        const uint64_t c = ((uint64_t)i * L + lane) * N;
-        if (c < a.dim)
-            store_vec<float, N>(a.part_w + slot * a.dim + c, dw[i], (int64_t)(a.dim - c));
+        for (int i = 0; i < Ch; ++i) {
+            const uint64_t c = ((uint64_t)i * L + lane) * N;
+            if (c < a.dim)
+                store_vec<float, N>(pw + c, dw[i], (int64_t)(a.dim - c));
+        }
+    } else {
+        __shared__ float share[Per][Ch * L * N];
+#pragma unroll
+        for (int i = 0; i < Ch; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                share[threadIdx.x / L][(i * L + lane) * N + j] = dw[i][j];
+        __syncthreads();
+        for (uint32_t c = threadIdx.x; c < a.dim; c += Threads) {
+            float sum = share[0][c];
+#pragma unroll
+            for (uint32_t p = 1; p < Per; ++p)
+                sum += share[p][c];
+            pw[c] = sum;
+        }
     }
 }
 
-// Long rows: read twice; the slot's share of dw lives in its workspace row
+// Long rows: read twice; the workgroup's share of dw lives in its workspace row
 // (each element is always the same lane's).
 template <typename T>
 __global__ __launch_bounds__(1024) void rms_norm_grad_long_kernel(RmsGrad a)
@@ -333,7 +350,7 @@ __global__ __launch_bounds__(1024) void rms_norm_grad_long_kernel(RmsGrad a)
     const uint64_t slot = blockIdx.x, step = (uint64_t)L * N, c0 = (uint64_t)threadIdx.x * N;
     float *pw = a.part_w + slot * a.dim;
     uint32_t turn = 0;
-    for (uint64_t row = slot; row < a.rows; row += a.slots, turn ^= 1u) {
+    for (uint64_t row = slot; row < a.rows; row += a.groups, turn ^= 1u) {
         const T *dy = (const T *)a.dy + row * a.dy_ld, *h = (const T *)a.h + row * a.h_ld;
         const T *dh = (const T *)a.dh + row * a.dh_ld;
         const float rstd = a.rstd[row];
@@ -370,12 +387,12 @@ __global__ __launch_bounds__(1024) void rms_norm_grad_long_kernel(RmsGrad a)
     }
 }
 
-// dw[c] (+)= the slots' shares: 32 columns per workgroup, 32 groups of lanes
-// over every 32nd slot, their sums in order.  (64 columns and 16 groups leave
+// dw[c] (+)= the shares: 32 columns per workgroup, 32 groups of lanes over every
+// 32nd share, their sums in order.  (64 columns and 16 groups leave
 // half the compute units idle at 4096 columns; 16 columns use half a line.)
 constexpr uint32_t kDwThreads = 1024, kDwCols = 32;
 __global__ __launch_bounds__(kDwThreads) void rms_norm_dw_kernel(const float *__restrict__ part_w,
-                                                                 uint64_t slots, uint64_t dim,
+                                                                 uint64_t shares, uint64_t dim,
                                                                  float *__restrict__ dw, bool add)
 {
     constexpr uint32_t groups = kDwThreads / kDwCols;
@@ -385,7 +402,7 @@ __global__ __launch_bounds__(kDwThreads) void rms_norm_dw_kernel(const float *__
     float sum = 0.0f;
     if (c < dim) {
 #pragma unroll 8
-        for (uint64_t s = group; s < slots; s += groups)
+        for (uint64_t s = group; s < shares; s += groups)
             sum += part_w[s * dim + c];
     }
     share[group][lane] = sum;
@@ -405,12 +422,15 @@ struct Split {
 };
 
 template <typename T>
-Split split_row(uint64_t dim, uint64_t most, bool half = false)   // half: 512 lanes, too
+Split split_row(uint64_t dim, uint64_t most, bool q8 = false)
 {
     const uint64_t vecs = (dim + kVec<T> - 1) / kVec<T>;
-    for (int lanes : {64, 256, 512}) {
+    for (int lanes : {16, 64, 256, 512}) {
         const uint64_t ch = (vecs + lanes - 1) / lanes;
-        if (ch <= most && (lanes < 512 || half))
+        // 16 lanes: two vectors at most (three for 60000 x 384 bf16 35 us, one of
+        // 64 lanes 33), and 128 columns at once where a group may be as many
+        if (lanes == 16 ? ch <= 2 && ch <= most && (!q8 || kVec<T> == 8)
+                        : ch <= most && (lanes < 512 || q8))
             return {lanes, (int)ch};
     }
     return {1024, vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 && sizeof(T) == 4 ? 4 : 0};
@@ -435,14 +455,15 @@ void norm(const RmsNorm &a, int ch, hipStream_t s)
         norm<T, L, 1, Q8>(a, s);
     else if (ch == 2)
         norm<T, L, 2, Q8>(a, s);
-    else if constexpr (L < 1024 && !Q8)
+    else if constexpr ((L == 64 || L == 256) && !Q8)
         norm<T, L, 3, Q8>(a, s);
     else if constexpr (L == 1024 && sizeof(T) == 4)
         norm<T, L, 4, Q8>(a, s);
 }
 
-// Many rows get up to three vectors a lane, to 8 bits two and 512 lanes before
-// 1024, us: to 8 bits 16000 x 5120 bf16 121 with two of 512 lanes, 153 with
+// Short rows share a wavefront: 16 lanes each (60000 x 64 bf16 8.7 us, 64 lanes
+// 20).  Many rows get up to three vectors a lane, to 8 bits two and 512 lanes
+// before 1024, us: to 8 bits 16000 x 5120 bf16 121 with two of 512 lanes, 153 with
 // three of 256; 8192 x 8192 81, one of 1024 lanes 86; plain, 112 and 112, 90
 // and 87; 2999 x 2051 float32 plain 10.4 with three of 256 lanes, 14.5 with one
 // of 1024.
@@ -458,8 +479,12 @@ void norm(const RmsNorm &a, hipStream_t s)
         norm<T, 256, Q8>(a, p.ch, s);
     else if (p.lanes == 1024)
         norm<T, 1024, Q8>(a, p.ch, s);
-    else if constexpr (Q8)
-        norm<T, 512, Q8>(a, p.ch, s);
+    else if (p.lanes == 512) {
+        if constexpr (Q8)
+            norm<T, 512, Q8>(a, p.ch, s);
+    } else if constexpr (!Q8 || kVec<T> == 8) {
+        norm<T, 16, Q8>(a, p.ch, s);
+    }
 }
 
 // The gradient's rows: two vectors a lane at most, 16-bit ones three of 256
@@ -473,25 +498,27 @@ Split grad_split(uint64_t dim)
     return p.lanes == 1024 && sizeof(T) == 2 && dim <= 3 * 256 * kVec<T> ? Split{256, 3} : p;
 }
 
-// Slots of the gradient: what is resident at once, few enough that their shares
-// of dw are a small part of the traffic (16384 x 4096 bf16, us for 512 / 768 /
-// 1024 / 1536 slots of 256 lanes: 109 / 101 / 101 / 109; 16000 x 5120, three
-// vectors a lane, 768 / 1024: 127 / 156; 1024 lanes, 256 / 512 slots: 8192 x
-// 8192 bf16 107 / 111, 8192 x 4096 float32 99 / 94).
+// Short rows share a wavefront here, too (60000 x 64 bf16 13 us, 64 lanes each
+// 25).  Workgroups of the gradient: what is resident at once, few enough that their
+// shares of dw are a small part of the traffic (16384 x 4096 bf16, us for 512 /
+// 768 / 1024 / 1536 of 256 lanes: 109 / 101 / 101 / 109; 16000 x 5120, three
+// vectors a lane, 768 / 1024: 127 / 156; 1024 lanes, 256 / 512: 8192 x 8192
+// bf16 107 / 111, 8192 x 4096 float32 99 / 94).
 template <typename T>
-uint64_t grad_slots(uint64_t rows, Split p)
+uint64_t grad_groups(uint64_t rows, Split p)
 {
-    const uint64_t most = p.lanes == 64    ? 4096
+    const uint64_t most = p.lanes < 256    ? 1024
                           : p.lanes == 256 ? (p.ch == 3 ? 768 : 1024)
                                            : (p.ch * kVec<T> == 4 ? 512 : 256);
-    return rows < most ? rows : most;
+    const uint64_t per = p.lanes < 256 ? 256 / p.lanes : 1, all = (rows + per - 1) / per;
+    return all < most ? all : most;
 }
 
 template <typename T, int L, int Ch>
 void norm_grad(const RmsGrad &a, hipStream_t s)
 {
-    constexpr int threads = L < 256 ? 256 : L, per = threads / L;
-    const uint32_t grid = (uint32_t)((a.slots + per - 1) / per);
+    constexpr int threads = L < 256 ? 256 : L;
+    const uint32_t grid = (uint32_t)a.groups;
     // from 64 MiB a matrix on: 16384 x 4096 bf16 101 us against 104, but 2048 x
     // 4096 (16 MiB) 26 against 21
     if (a.rows * a.dim * sizeof(T) >= (64ull << 20))
@@ -517,10 +544,12 @@ template <typename T>
 hipError_t norm_grad(RmsGrad a, hipStream_t s)
 {
     const Split p = grad_split<T>(a.dim);
-    a.slots = grad_slots<T>(a.rows, p);
+    a.groups = grad_groups<T>(a.rows, p);
     if (a.rows) {
         if (!p.ch)
-            rms_norm_grad_long_kernel<T><<<(uint32_t)a.slots, 1024, 0, s>>>(a);
+            rms_norm_grad_long_kernel<T><<<(uint32_t)a.groups, 1024, 0, s>>>(a);
+        else if (p.lanes == 16)
+            norm_grad<T, 16>(a, p.ch, s);
         else if (p.lanes == 64)
             norm_grad<T, 64>(a, p.ch, s);
         else if (p.lanes == 256)
@@ -529,7 +558,7 @@ hipError_t norm_grad(RmsGrad a, hipStream_t s)
             norm_grad<T, 1024>(a, p.ch, s);
     }
     rms_norm_dw_kernel<<<(uint32_t)((a.dim + kDwCols - 1) / kDwCols), kDwThreads, 0, s>>>(
-        a.part_w, a.slots, a.dim, a.dw, a.add);
+        a.part_w, a.groups, a.dim, a.dw, a.add);
     return hipGetLastError();
 }
 
@@ -537,8 +566,8 @@ hipError_t norm_grad(RmsGrad a, hipStream_t s)
 
 uint64_t rms_norm_work_bytes(uint64_t rows, uint64_t dim, int type)
 {
-    return 4 * dim * (type == GCQ_F32 ? grad_slots<float>(rows, grad_split<float>(dim))
-                                      : grad_slots<_Float16>(rows, grad_split<_Float16>(dim)));
+    return 4 * dim * (type == GCQ_F32 ? grad_groups<float>(rows, grad_split<float>(dim))
+                                      : grad_groups<_Float16>(rows, grad_split<_Float16>(dim)));
 }
 
 hipError_t launch_rms_norm(const RmsNorm &a, hipStream_t stream)

@@ -21,7 +21,7 @@ EPS = 1e-5
 
 SHAPES = [(1, 1), (3, 7), (5, 64), (4, 100), (2, 511), (7, 513), (3, 1025), (1, 2048), (2, 4100),
           (1030, 40), (1025, 1030), (2, 8192), (3, 8197), (2, 16384), (2, 16389), (2, 33001),
-          (3, 2500)]
+          (3, 2500), (1030, 200), (1100, 65)]
 
 
 def dtype(name):
@@ -233,10 +233,10 @@ def test_norm_grad(gpu, kind, w32, with_dh):
             assert torch.equal(dx3, dx)
 
 
-# three vectors a lane (64 and 256 lanes), two of 512 lanes to 8 bits, and
+# rows that share a wavefront, three vectors a lane (64 and 256 lanes), two of 512 lanes to 8 bits, and
 # matrices past the sizes from
 # which accesses are non-temporal
-MANY = [(1030, 700), (1025, 1400), (1025, 2500), (1025, 5000), (9000, 4100)]
+MANY = [(1030, 200), (20001, 100), (5000, 65), (1030, 700), (1025, 1400), (1025, 2500), (1025, 5000), (9000, 4100)]
 
 
 @pytest.mark.parametrize("kind", TYPES)
