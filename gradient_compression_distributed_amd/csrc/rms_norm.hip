@@ -433,7 +433,8 @@ Split split_row(uint64_t dim, uint64_t most, bool q8 = false)
                         : ch <= most && (lanes < 512 || q8))
             return {lanes, (int)ch};
     }
-    return {1024, vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 && sizeof(T) == 4 ? 4 : 0};
+    const uint64_t ch = (vecs + 1023) / 1024;
+    return {1024, ch <= 16 / kVec<T> ? (int)ch : 0};
 }
 
 template <typename T, int L, int Ch, bool Q8>
@@ -458,7 +459,7 @@ void norm(const RmsNorm &a, int ch, hipStream_t s)
     else if constexpr ((L == 64 || L == 256) && !Q8)
         norm<T, L, 3, Q8>(a, s);
     else if constexpr (L == 1024 && sizeof(T) == 4)
-        norm<T, L, 4, Q8>(a, s);
+        ch == 3 ? norm<T, L, 3, Q8>(a, s) : norm<T, L, 4, Q8>(a, s);
 }
 
 // Short rows share a wavefront: 16 lanes each (60000 x 64 bf16 8.7 us, 64 lanes
@@ -466,7 +467,8 @@ void norm(const RmsNorm &a, int ch, hipStream_t s)
 // before 1024, us: to 8 bits 16000 x 5120 bf16 121 with two of 512 lanes, 153 with
 // three of 256; 8192 x 8192 81, one of 1024 lanes 86; plain, 112 and 112, 90
 // and 87; 2999 x 2051 float32 plain 10.4 with three of 256 lanes, 14.5 with one
-// of 1024.
+// of 1024; 5500 x 12000 float32 to 8 bits 173 with three of 1024, 211 with four
+// of which one is idle.
 template <typename T, bool Q8>
 void norm(const RmsNorm &a, hipStream_t s)
 {
@@ -537,7 +539,7 @@ void norm_grad(const RmsGrad &a, int ch, hipStream_t s)
     else if constexpr (L == 256 && sizeof(T) == 2)
         norm_grad<T, L, 3>(a, s);
     else if constexpr (L == 1024 && sizeof(T) == 4)
-        norm_grad<T, L, 4>(a, s);
+        ch == 3 ? norm_grad<T, L, 3>(a, s) : norm_grad<T, L, 4>(a, s);
 }
 
 template <typename T>

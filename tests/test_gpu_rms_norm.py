@@ -236,7 +236,7 @@ def test_norm_grad(gpu, kind, w32, with_dh):
 # rows that share a wavefront, three vectors a lane (64 and 256 lanes), two of 512 lanes to 8 bits, and
 # matrices past the sizes from
 # which accesses are non-temporal
-MANY = [(1030, 200), (20001, 100), (5000, 65), (1030, 700), (1025, 1400), (1025, 2500), (1025, 5000), (9000, 4100)]
+MANY = [(1100, 9000), (1030, 200), (20001, 100), (5000, 65), (1030, 700), (1025, 1400), (1025, 2500), (1025, 5000), (9000, 4100)]
 
 
 @pytest.mark.parametrize("kind", TYPES)
