@@ -139,7 +139,9 @@ def test_rms_norm_grad(lib):
         (dict(dx=A), E_OVERLAP), (dict(dx=A + MB), E_OVERLAP), (dict(dx=A + 4 * MB, dx_ld=9), E_OVERLAP),
         (dict(dw=A + 2 * MB), E_OVERLAP), (dict(work=A + 6 * MB), E_OVERLAP),
         (dict(rows=0, add=1, dy=0, h=0, w=0, rstd=0, dx=0, work=0), OK)])
-    assert lib.rms_norm_work_bytes(10, 8, F16) == 10 * 8 * 4
+    # a row of sums per workgroup, which 16 rows of up to 256 columns share
+    assert lib.rms_norm_work_bytes(10, 8, F16) == 8 * 4
+    assert lib.rms_norm_work_bytes(33, 256, F16) == 3 * 256 * 4
     assert lib.rms_norm_work_bytes(10, 8, I32) == 0
 
 
