@@ -78,20 +78,40 @@ __device__ __forceinline__ void store_codes(uint8_t *p, fvec<N> v, int64_t left)
     store_vec<uint8_t, N>(p, b, left);
 }
 
-// Scale of a group whose largest magnitude is a, and the factor that takes
-// values to codes (one division per group; the factor's rounding can move a
-// value within 2^-23 of a tie to its other neighbour).
-__device__ __forceinline__ float group_scale(float a, float &inv)
+// How a group's values become codes: its scale and 1 / scale, 0 for a scale of
+// 0.
+struct Scale {
+    float s, inv;
+};
+
+// Scale of a group whose largest magnitude is a.
+__device__ __forceinline__ Scale group_scale(float a)
 {
     const float s = a == 0.0f ? 0.0f : fmaxf(a / kE4m3Max, kMinNormal);
-    inv = s == 0.0f ? 0.0f : 1.0f / s;
-    return s;
+    return {s, s == 0.0f ? 0.0f : 1.0f / s};
+}
+
+// y / scale in float32.  The product with the rounded reciprocal misses one tie
+// between two codes in eight (129000 of scales 3 .. 2047); its remainder's
+// correction (Markstein 1990) makes it the rounded quotient, with two
+// operations a value and one division a group.  A scale of infinity leaves
+// finite values 0 (their remainder would be NaN).
+template <int N>
+__device__ __forceinline__ fvec<N> quotient(fvec<N> y, Scale g)
+{
+    const float s = __builtin_isinf(g.s) ? 0.0f : g.s;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float q = y[j] * g.inv;
+        y[j] = fmaf(-fmaf(q, s, -y[j]), g.inv, q);
+    }
+    return y;
 }
 
 // A row's lanes hold Ch vectors of N columns, L * N columns apart.  Nt: x, the
 // residual, h and y by non-temporal accesses; the codes are always stored
 // ordinarily (non-temporal ones are slower).  Bound by memory: 16384 x 4096
-// bf16 with a residual to 8 bits 80 us (472 MB, 5.9 TB/s); few rows take a
+// bf16 with a residual to 8 bits 81 us (472 MB, 5.8 TB/s); few rows take a
 // launch (8192 columns on 1024 lanes, 4 us).
 template <typename T, int L, int Ch, bool Q8, bool Nt>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_kernel(RmsNorm a)
@@ -144,27 +164,27 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_kernel(RmsNorm a)
             if (a.group) {   // a group is the columns of group / N neighbouring lanes
                 for (uint32_t o = 1; o * N < a.group; o <<= 1)
                     m = fmaxf(m, __shfl_xor(m, (int)o, kWave));
-                float inv;
-                const float s = group_scale(m, inv);
+                const Scale g = group_scale(m);
                 if (c < a.dim) {
                     if (c % a.group == 0)
-                        a.scales[row * a.parts + c / a.group] = s;
-                    store_codes<N>(a.codes + row * a.y_ld + c, h[i] * inv, (int64_t)(a.dim - c));
+                        a.scales[row * a.parts + c / a.group] = g.s;
+                    store_codes<N>(a.codes + row * a.y_ld + c, quotient<N>(h[i], g),
+                                   (int64_t)(a.dim - c));
                 }
             }
         }
     }
     if constexpr (Q8) {
         if (!a.group) {
-            float inv;
-            const float s = group_scale(row_reduce<L, true>(top, part[1]), inv);
+            const Scale g = group_scale(row_reduce<L, true>(top, part[1]));
             if (lane == 0)
-                a.scales[row] = s;
+                a.scales[row] = g.s;
 #pragma unroll
             for (int i = 0; i < Ch; ++i) {
                 const uint64_t c = ((uint64_t)i * L + lane) * N;
                 if (c < a.dim)
-                    store_codes<N>(a.codes + row * a.y_ld + c, h[i] * inv, (int64_t)(a.dim - c));
+                    store_codes<N>(a.codes + row * a.y_ld + c, quotient<N>(h[i], g),
+                                   (int64_t)(a.dim - c));
             }
         }
     }
@@ -200,7 +220,7 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNorm a)
     const float rstd = 1.0f / sqrtf(sum / (float)a.dim + a.eps);
     if (a.rstd && threadIdx.x == 0)
         a.rstd[row] = rstd;
-    float inv = 0.0f;
+    Scale g = {0.0f, 0.0f};
     if constexpr (Q8) {
         if (!a.group) {
             float top = 0.0f;
@@ -211,9 +231,9 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNorm a)
                 for (int j = 0; j < N; ++j)
                     top = fmaxf(top, fabsf(y[j]));
             }
-            const float s = group_scale(row_reduce<L, true>(top, part[1]), inv);
+            g = group_scale(row_reduce<L, true>(top, part[1]));
             if (threadIdx.x == 0)
-                a.scales[row] = s;
+                a.scales[row] = g.s;
         }
     }
     // every lane takes part in a group's maximum: whole steps
@@ -237,12 +257,12 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNorm a)
                     m = fmaxf(m, fabsf(y[j]));
                 for (uint32_t o = 1; o * N < a.group; o <<= 1)
                     m = fmaxf(m, __shfl_xor(m, (int)o, kWave));
-                const float s = group_scale(m, inv);
+                g = group_scale(m);
                 if (left > 0 && c % a.group == 0)
-                    a.scales[row * a.parts + c / a.group] = s;
+                    a.scales[row * a.parts + c / a.group] = g.s;
             }
             if (left > 0)
-                store_codes<N>(a.codes + row * a.y_ld + c, y * inv, left);
+                store_codes<N>(a.codes + row * a.y_ld + c, quotient<N>(y, g), left);
         }
     }
 }

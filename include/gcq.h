@@ -565,8 +565,8 @@ int rms_norm(const void *x, int type, size_t rows, size_t dim, size_t x_ld, cons
  * shorter), as qsgd_quantize_maxnorm scales its buckets:
  *     a = max |y| over the group, a NaN never becoming the maximum
  *     scale = 0 if a = 0, else max(a / 448, 2^-126)
- *     code = y * (1 / scale) to the nearest OCP e4m3 value, ties to even
- *            (0 where scale = 0, NaN for a NaN)
+ *     code = y / scale, rounded to float32 and then to the nearest OCP e4m3
+ *            value, ties to even (0 where scale = 0, NaN for a NaN)
  * so y is about scale * code.  Nothing overflows: 448 is e4m3's largest.
  *
  *   group   32, 64 or 128; 0: the whole row
