@@ -10,6 +10,8 @@
 // add in an order that changes from call to call; here the positions are
 // sorted by token first (a stable radix sort, so equal tokens keep their
 // order), and every sum runs over sorted positions in a fixed order.
+#include <algorithm>
+
 #include "gcq_device.h"
 #include "gcq_lm.h"
 
@@ -865,28 +867,44 @@ uint64_t up256(uint64_t x) { return (x + 255) / 256 * 256; }
 // are too few to give the device 4096 wavefronts of 256 columns.  All positions
 // in one run need no join: sorting and summing 20 positions of 512 columns
 // takes 16.8 us from the host so, 20.1 with runs of 8 and a join.
+constexpr uint64_t kFullWaves = 4096;
+constexpr uint32_t kLeastRun = 8;
 uint32_t run_length(uint64_t n, uint64_t dim)
 {
     uint32_t r = kEmbedRun;
-    while (n > kEmbedRun && r > 8 && (n + r - 1) / r * ((dim + 255) / 256) < 4096)
+    while (n > kEmbedRun && r > kLeastRun && (n + r - 1) / r * ((dim + 255) / 256) < kFullWaves)
         r /= 2;
     return r;
 }
 
-// Where the workspace's parts begin.
+// The workspace's parts: the runs' segment starts, the tiles' counts, two rows
+// of open sums a run.
 struct WorkLayout {
-    uint64_t tiles, part, bytes;
+    uint64_t tiles, part;   // where they begin
 };
 
 WorkLayout work_layout(uint64_t n, uint64_t dim)
 {
     const uint32_t r = run_length(n, dim);
     const uint64_t runs = (n + r - 1) / r, tiles = (n + kEmbedTile - 1) / kEmbedTile;
-    WorkLayout w;
-    w.tiles = up256(4 * runs);
-    w.part = w.tiles + up256(4 * (tiles + 1));
-    w.bytes = w.part + 8 * runs * dim;
-    return w;
+    const uint64_t at = up256(4 * runs);
+    return {at, at + up256(4 * (tiles + 1))};
+}
+
+// The most that any call of up to n positions and dim columns needs, so a
+// workspace for the largest batch serves every other one: shorter runs make
+// more sums of fewer positions (16000 x 2048 twice as many as 16384 x 2048).
+// Runs are shorter than kEmbedRun only while runs twice as long times the
+// groups of 256 columns are less than kFullWaves, so there are then less than
+// 2 * kFullWaves of runs times groups.
+uint64_t most_work(uint64_t n, uint64_t dim)
+{
+    const uint64_t tiles = (n + kEmbedTile - 1) / kEmbedTile;
+    const uint64_t longest = (n + kEmbedRun - 1) / kEmbedRun;
+    const uint64_t shortest = n <= kEmbedRun ? longest : (n + kLeastRun - 1) / kLeastRun;
+    const uint64_t runs = std::max(longest, std::min(shortest, 2 * kFullWaves));
+    const uint64_t sums = std::max(longest * dim, std::min(shortest * dim, 2 * kFullWaves * 256));
+    return up256(4 * runs) + up256(4 * (tiles + 1)) + 8 * sums;
 }
 
 }  // namespace
@@ -897,7 +915,7 @@ uint64_t embed_plan_words(uint64_t n)
     return n <= kCountSort ? 2 * n : 4 * n + (tiles + 1) * kBins;
 }
 
-uint64_t embed_work_bytes(uint64_t n, uint64_t dim) { return work_layout(n, dim).bytes; }
+uint64_t embed_work_bytes(uint64_t n, uint64_t dim) { return most_work(n, dim); }
 
 void embed_work_layout(EmbedGrad &e, void *work)
 {

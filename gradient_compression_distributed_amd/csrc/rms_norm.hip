@@ -14,6 +14,8 @@
 // A row stays in the registers of the lanes that share it between the pass
 // for its statistics and the pass that uses them, so every matrix is read
 // once.  Statistics are taken from h before it is rounded for storing.
+#include <algorithm>
+
 #include "gcq_device.h"
 #include "gcq_lm.h"
 
@@ -536,6 +538,23 @@ uint64_t grad_groups(uint64_t rows, Split p)
     return all < most ? all : most;
 }
 
+// The most that any call of up to `rows` rows of up to `dim` columns needs, so
+// a workspace for the largest serves every other one: shorter rows have more
+// workgroups (16-bit rows of 4096 columns 1024, of 8192 256).  The workgroups
+// depend on dim by its split alone, so each split needs the most at the longest
+// row that it takes, in vectors: 2 of 16, 64 and 256 lanes, 3 of 256, 1 of 1024.
+template <typename T>
+uint64_t most_work(uint64_t rows, uint64_t dim)
+{
+    uint64_t most = dim * grad_groups<T>(rows, grad_split<T>(dim));
+    for (uint64_t vecs : {32, 128, 512, 768, 1024}) {
+        const uint64_t d = vecs * kVec<T>;
+        if (d < dim)
+            most = std::max(most, d * grad_groups<T>(rows, grad_split<T>(d)));
+    }
+    return 4 * most;
+}
+
 template <typename T, int L, int Ch>
 void norm_grad(const RmsGrad &a, hipStream_t s)
 {
@@ -588,8 +607,7 @@ hipError_t norm_grad(RmsGrad a, hipStream_t s)
 
 uint64_t rms_norm_work_bytes(uint64_t rows, uint64_t dim, int type)
 {
-    return 4 * dim * (type == GCQ_F32 ? grad_groups<float>(rows, grad_split<float>(dim))
-                                      : grad_groups<_Float16>(rows, grad_split<_Float16>(dim)));
+    return type == GCQ_F32 ? most_work<float>(rows, dim) : most_work<_Float16>(rows, dim);
 }
 
 hipError_t launch_rms_norm(const RmsNorm &a, hipStream_t stream)

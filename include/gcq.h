@@ -500,7 +500,8 @@ int embed_sort(const void *tokens, int token_type, size_t n, size_t vocab, uint3
  *   plan    in,     from embed_sort with this n and vocab
  *   dtable  in/out, float32, vocab x dim, rows dtable_ld apart
  *   work    embed_work_bytes(n, dim) bytes, 16-byte aligned, contents not
- *           kept; calls that may run at the same time need one each
+ *           kept; calls that may run at the same time need one each.  The size
+ *           never falls with n or dim, so one for the largest serves them all
  *
  * n == 0 without accumulate zeroes dtable.
  * Errors: as embed_lookup.
@@ -594,7 +595,8 @@ int rms_norm_q8(const void *x, int type, size_t rows, size_t dim, size_t x_ld,
  *   dweight    out, float32[dim]
  *   work       rms_norm_work_bytes(rows, dim, type) bytes, 16-byte aligned,
  *              contents not kept; calls that may run at the same time need
- *              one each
+ *              one each.  The size never falls with rows or dim, so one for
+ *              the largest of a type serves them all
  *
  * rows == 0 without accumulate zeroes dweight.
  * Errors: as rms_norm.
@@ -679,12 +681,14 @@ size_t qsgd_elias_max_words(size_t n, uint32_t d);
 size_t saps_mask_words(size_t n);
 /* ceil(n/8192): SAPS tiles (saps_mask writes one more offset than this). */
 size_t saps_num_tiles(size_t n);
-/* Words of an embed_sort plan (0 for n above GCQ_LM_MAX_ROWS). */
+/* Words of an embed_sort plan (0 for n above GCQ_LM_MAX_ROWS), never fewer for
+ * more positions. */
 size_t embed_plan_words(size_t n);
 /* Bytes of embed_grad's and embed_grad_rows' workspace (0 for sizes out of
- * range). */
+ * range), never fewer for a larger n or dim. */
 size_t embed_work_bytes(size_t n, size_t dim);
-/* Bytes of rms_norm_grad's workspace (0 for sizes or types out of range). */
+/* Bytes of rms_norm_grad's workspace (0 for sizes or types out of range), never
+ * fewer for more rows or a larger dim of the same type. */
 size_t rms_norm_work_bytes(size_t rows, size_t dim, int type);
 /* Static, never-NULL name of a status code. */
 const char *gcq_status_string(int status);
