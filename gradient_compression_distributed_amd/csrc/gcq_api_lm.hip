@@ -319,7 +319,9 @@ bool topk_ok(size_t rows, size_t vocab, uint32_t k, int type, int idx_type, int 
 {
     return rows_of(rows) && vocab >= 1 && vocab <= GCQ_LM_MAX_DIM && k >= 1 && k <= GCQ_MAX_TOPK &&
            float_type(type) && index_type(idx_type) && (top_type == type || top_type == GCQ_F32) &&
-           isfinite(t) && t > 0.0f && isfinite(scale);
+           isfinite(t) && t > 0.0f && isfinite(scale) &&
+           // the kernels' factors; an infinite one gives NaN at a row's largest logit
+           isfinite(1.44269504f / t) && isfinite(scale / t);
 }
 
 // Everything that the three calls share: `lse_in` for the gradient alone,

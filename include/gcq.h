@@ -630,7 +630,8 @@ int rms_norm_grad(const void *dy, int type, size_t rows, size_t dim, size_t dy_l
  *   index      in,  rows x k of index_type (GCQ_I32 or GCQ_I64)
  *   teacher    in,  rows x k of teacher_type: `type` or GCQ_F32
  *   k          1 .. GCQ_MAX_TOPK
- *   T          finite and > 0;  scale finite
+ *   T          finite and > 0, log2(e) / T and scale / T finite in float32 (T
+ *              is then above 4.2e-39);  scale finite
  *   row_scale  in,  float32[rows], or NULL: a mask, a weight, or the
  *              gradient that comes from above
  *   loss, lse  out, float32[rows]
