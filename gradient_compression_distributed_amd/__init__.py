@@ -9,6 +9,12 @@ missing, ``load()`` raises.
 
 Packed words (2-bit codes, QSGD nibbles) are held in ``torch.int32``
 tensors as raw 32-bit patterns (view them as uint32 on the host).
+
+No call records anything for autograd.  The language-model operators refuse
+tensors that require a gradient while gradients are recorded (call them under
+``torch.no_grad()``, in a ``torch.autograd.Function``, or with detached
+tensors), and raise the version of what they write, as torch's own in-place
+operations do.
 """
 from __future__ import annotations
 
@@ -559,14 +565,18 @@ def qsgd_elias_decode(words, offsets, n: int, d: int, norms=None, nibbles=None):
 # Matrices are 2-D tensors whose rows are contiguous; rows may lie further
 # apart than their length (a slice of columns).  A call runs on the device of
 # its tensors, on that device's current stream, whatever device is current.
+# Calls record nothing for autograd: where gradients are recorded, a tensor that
+# requires one is refused (its gradient would be lost without a word), and the
+# version of every tensor that a call writes is raised, so that a backward pass
+# that saved it before says so.
 # What a call needs of torch, looked up once (by _lm): the small calls take a
 # few microseconds, and an import statement or a Stream object is a part of it.
-_torch = _tensor = _type_codes = _raw_stream = _current_device = None
+_torch = _tensor = _type_codes = _raw_stream = _current_device = _wrote = None
 
 
 def _lm():
     """The library, with the names above set."""
-    global _torch, _tensor, _type_codes, _raw_stream, _current_device
+    global _torch, _tensor, _type_codes, _raw_stream, _current_device, _wrote
     if _torch is None:
         import torch
 
@@ -576,6 +586,7 @@ def _lm():
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
         _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _wrote = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
         _torch, _tensor = torch, torch.Tensor
     return _lib if _lib is not None else load()
 
@@ -589,12 +600,16 @@ def _type_code(x, name, allowed=(0, 1, 2)):
 
 
 def _on(x, name, device=None):
-    """Refuses what is not a GPU tensor (on ``device``, an index, if given);
-    returns the index of its device."""
+    """Refuses what is not a GPU tensor (on ``device``, an index, if given) and
+    one whose gradient would be lost; returns the index of its device."""
     try:
         at = x.get_device()
+        lost = x.requires_grad
     except AttributeError:
         raise TypeError(f"{name} must be a torch tensor") from None
+    if lost and _torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call does not record: call it "
+                         "under torch.no_grad() or in a torch.autograd.Function, or detach it")
     if at < 0:
         raise ValueError(f"{name} must live in GPU memory (got {x.device})")
     if device is not None and at != device:
@@ -628,7 +643,7 @@ def _first(x, name):
 def _matrix(x, name, rows, cols, device, written=False):
     """Checks a matrix of rows x cols (at least ``rows`` rows if it is
     written); returns the distance of its rows in elements."""
-    if type(x) is not _tensor or x.get_device() != device:
+    if type(x) is not _tensor or x.get_device() != device or x.requires_grad:
         _on(x, name, device)
     shape = x.shape
     if shape != (rows, cols) and (len(shape) != 2 or shape[1] != cols or not written or shape[0] < rows):
@@ -639,7 +654,7 @@ def _matrix(x, name, rows, cols, device, written=False):
 def _vector(x, name, n, device, dtype=None, at_least=False):
     """Checks a contiguous tensor of n elements (or at least n, or any number
     for None); returns how many it holds."""
-    if type(x) is not _tensor or x.get_device() != device:
+    if type(x) is not _tensor or x.get_device() != device or x.requires_grad:
         _on(x, name, device)
     if dtype is not None and x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {x.dtype})")
@@ -683,6 +698,7 @@ def embed_lookup(table, tokens, scale: float = 1.0, out=None):
     _call(lib.embed_lookup, "embed_lookup", dev, table.data_ptr(), _type_code(table, "table"),
           vocab, dim, ld, tokens.data_ptr(), _type_code(tokens, "tokens", (3, 4)), n, scale,
           out.data_ptr(), _type_code(out, "out"), out_ld)
+    _wrote((out,))
     return out
 
 
@@ -709,6 +725,7 @@ def embed_sort(tokens, vocab: int, plan=None) -> EmbedPlan:
     _call(lib.embed_sort, "embed_sort", dev, tokens.data_ptr(),
           _type_code(tokens, "tokens", (3, 4)), n, vocab, plan.words.data_ptr())
     plan.vocab = vocab
+    _wrote((plan.words,))
     return plan
 
 
@@ -746,6 +763,7 @@ def embed_grad(grad, plan: EmbedPlan, scale: float = 1.0, out=None, accumulate: 
     _call(lib.embed_grad, "embed_grad", dev, grad.data_ptr(), _type_code(grad, "grad"), ld,
           plan.words.data_ptr(), plan.n, plan.vocab, dim, scale, accumulate, out.data_ptr(), out_ld,
           work.data_ptr())
+    _wrote((out,))
     return out
 
 
@@ -771,6 +789,7 @@ def embed_grad_rows(grad, plan: EmbedPlan, scale: float = 1.0, ids=None, rows=No
     _call(lib.embed_grad_rows, "embed_grad_rows", dev, grad.data_ptr(), _type_code(grad, "grad"),
           ld, plan.words.data_ptr(), plan.n, plan.vocab, dim, scale, ids.data_ptr(),
           rows.data_ptr(), rows_ld, count.data_ptr(), work.data_ptr())
+    _wrote((ids, rows, count))
     return ids, rows, count
 
 
@@ -822,6 +841,7 @@ def rms_norm(x, weight, eps: float, residual=None, y=None, h=None, rstd=None):
     y_ld = _matrix(y, "y", rows, dim, dev)
     _type_code(y, "y", (kind,))
     _call(lib.rms_norm, "rms_norm", dev, *args, eps, y.data_ptr(), y_ld, *tail)
+    _wrote((y, rstd) if residual is None else (y, rstd, h))
     return y, h, rstd
 
 
@@ -845,6 +865,7 @@ def rms_norm_q8(x, weight, eps: float, group: int = 128, residual=None, codes=No
     _vector(scales, "scales", rows * parts, dev, torch.float32)
     _call(lib.rms_norm_q8, "rms_norm_q8", dev, *args, eps, group, codes.data_ptr(), codes_ld,
           scales.data_ptr(), *tail)
+    _wrote((codes, scales, rstd) if residual is None else (codes, scales, rstd, h))
     return codes, scales, h, rstd
 
 
@@ -882,6 +903,7 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None, dx=None, dweight=None, accumulat
     _call(lib.rms_norm_grad, "rms_norm_grad", dev, dy.data_ptr(), kind, rows, dim, ld, h.data_ptr(),
           h_ld, weight.data_ptr(), _type_code(weight, "weight", (kind, 0)), rstd.data_ptr(), dh_at,
           dh_ld, dx.data_ptr(), dx_ld, dweight.data_ptr(), accumulate, work.data_ptr())
+    _wrote((dx, dweight))
     return dx, dweight
 
 
@@ -932,6 +954,7 @@ def distill_loss(logits, index, teacher, temperature: float = 1.0, row_scale=Non
     loss = _row_floats(loss, "loss", rows, dev, logits)
     lse = _row_floats(lse, "lse", rows, dev, logits)
     _call(lib.distill_loss, "distill_loss", dev, *head, *tail, loss.data_ptr(), lse.data_ptr())
+    _wrote((loss, lse))
     return loss, lse
 
 
@@ -945,6 +968,7 @@ def distill_grad(logits, lse, index, teacher, temperature: float = 1.0, row_scal
     _vector(lse, "lse", rows, dev, torch.float32)
     out, ld = _dlogits(out, logits, rows, vocab, kind, dev)
     _call(lib.distill_grad, "distill_grad", dev, *head, lse.data_ptr(), *tail, out.data_ptr(), ld)
+    _wrote((out,))
     return out
 
 
@@ -960,4 +984,5 @@ def distill_loss_grad(logits, index, teacher, temperature: float = 1.0, row_scal
     out, ld = _dlogits(out, logits, rows, vocab, kind, dev)
     _call(lib.distill_loss_grad, "distill_loss_grad", dev, *head, *tail, loss.data_ptr(),
           lse.data_ptr(), out.data_ptr(), ld)
+    _wrote((loss, lse, out))
     return loss, lse, out
