@@ -13,7 +13,8 @@
 //
 // Sums of exponentials run over exp2((z - m) log2(e) / T) with a running
 // maximum m per lane, joined over the lanes: one pass over the row.
-// Differences are taken before the factor, so the largest terms are exact.
+// Differences are taken before the factor, whose rounding moves an exponent x
+// by 2^-24 x: the largest terms are exact, small ones off by a few of those.
 #include "gcq_device.h"
 #include "gcq_lm.h"
 
@@ -26,6 +27,8 @@ using namespace lm;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLowest = -3.40282347e38f;   // a finite start: -inf - -inf is NaN
 
+// The hardware's exponential, off by about a step; results below 2^-126 may
+// come out 0 (a probability that no float32 sum with 1 in it notices).
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // A running maximum m of logits and the sum s of exp2((z - m) * c).
@@ -361,14 +364,15 @@ __device__ __forceinline__ float reduce_get(const float *part)
 // Loss and lse, and with Grad dz too: a workgroup per row.  The entries'
 // loads travel while the row is summed.  Both passes together read the row
 // twice and write it once, and all of that goes through the fabric between
-// the compute units and the last cache, which bounds the call (3 GB at 7 TB/s
-// for 4096 x 131072 bf16; without the exponentials it took as long).  So each
-// thread keeps its own vectors of the row's first columns between the passes:
-// Held batches in registers (two workgroups of 512 then fill a compute unit),
-// those up to column `kept` in LDS.  LDS alone brought 423 -> 393 us there,
-// registers no more (5.6 TB/s of what has to move; a plain copy of that size
-// reaches 5.4), but 8192 x 50021 388 -> 347 and 2048 x 131072 float32 435 ->
-// 415; 8192 x 8000, all of it in LDS, 65 -> 56.
+// the compute units and the last cache (3 GB at 7 TB/s for 4096 x 131072 bf16;
+// without the exponentials it took as long).  So each thread keeps its own
+// vectors of the row's first columns between the passes: Held batches in
+// registers (two workgroups of 512 then fill a compute unit), those up to
+// column `kept` in LDS.  Every byte is then moved once: 2.1 GB at 5.1 to 5.3
+// TB/s there, where a plain copy of 512 MiB reaches 5.4.  Columns in LDS brought
+// 423 -> 393 us, and 65 -> 56 where they are the whole row (8192 x 8000);
+// registers beside them nothing more there, but 8192 x 50021 416 -> 374 and
+// 2048 x 131072 float32 456 -> 422.
 template <typename T, int Threads, int Held, bool Grad, bool Nt>
 __global__ __launch_bounds__(Threads, Held ? 4 : 8) void distill_loss_kernel(Distill a,
                                                                              uint64_t kept)
@@ -464,8 +468,10 @@ __global__ __launch_bounds__(Threads, Held ? 4 : 8) void distill_loss_kernel(Dis
 }
 
 // dz from a kept lse; `parts` workgroups share a row, `chunk` columns each.
-// The exponent is ((z - hi) - lo) log2(e) / T with hi + lo = lse T: exact
-// where q is large.  Whether the row has entries at all is known only after
+// The exponent is ((z - hi) - lo) log2(e) / T with hi + lo = lse T, so nothing
+// is lost beyond the rounding of lse itself to float32: q is off by up to
+// 2^-24 |lse| relative, and a row's gradient sums to that instead of 0.
+// Whether the row has entries at all is known only after
 // the dense pass; a row without is zeroed then.  Bound by memory: 4096 x 131072
 // bf16 336 us (2.1 GB, 6.2 TB/s).
 template <typename T, int Threads, bool Nt>
@@ -541,14 +547,18 @@ template <typename T>
 hipError_t loss(const Distill &a, hipStream_t s)
 {
     // A workgroup for a few vectors a lane.  Long rows get few, large
-    // workgroups: with many rows in flight at once they no longer stay in the
-    // caches between the two passes.  Loss and gradient in bf16, us with 64 /
-    // 256 / 512 / 1024 threads and nothing held: 8192 x 1000 19 / 32 / 57 /
-    // 146; 8192 x 8000 83 / 75 / 90 / 169; 8192 x 32000 300 / 242 / 224 / 278;
-    // 4096 x 131072 633 / 579 / 486 / 437.  Batches held in registers: 8192 x
-    // 16000 99 with one, 107 without; 8192 x 40000 249 with two, 244 without;
-    // 8192 x 50021 347 with three, 388 without; 4096 x 100000 303 with four,
-    // 311 with three.
+    // workgroups: with many rows in flight at once they no longer stay on the
+    // chip between the two passes.  Loss and gradient in bf16, us with 64 / 256
+    // / 512 / 1024 threads, the columns that fit in LDS and none in registers:
+    // 8192 x 1000 21 / 34 / 60 / 146; 8192 x 8000 73 / 66 / 90 / 169; 8192 x
+    // 32000 270 / 225 / 209 / 260; 4096 x 60000 274 / 233 / 218 / 207.  Batches
+    // in registers too: 8192 x 16000 with 256 threads 111 with one, 122 without;
+    // with 512 threads 8192 x 40000 261 with two, 259 without; 8192 x 50021 374
+    // with three, 416 without; 4096 x 100000 313 with four, 328 with three; 4096
+    // x 131072 402 with four, 438 without (1024 threads 396, but 2048 x 131072
+    // float32 445 against 422).  The loss alone with 64 / 256 / 512 / 1024: 8192
+    // x 1000 11 / 22 / 42 / 91; 8192 x 8000 29 / 39 / 53 / 95, but 128 x 32000
+    // 16 / 9.6 / 9.5 / 9.3; 4096 x 131072 162 / 157 / 155 / 150.
     const uint64_t bytes = a.vocab * sizeof(T);
     if (bytes <= 8192)
         a.dz ? loss_grad<T, 64, 0>(a, s) : loss<T, 64>(a, s);

@@ -28,8 +28,9 @@ using namespace lm;
 // of 8192 float32 131 us, by one workgroup each 145; with one vector a lane
 // 136).  The R tokens are loaded together and then the R rows' vectors, so a
 // row waits for one load, not for two in turn (32768 rows of 4096 bf16, us for
-// R = 1 / 2 / 4 / 8: 80 / 75 / 82 / 83).  Bound by the fabric: rows of frequent tokens come from the last cache,
-// 268 MB out and as much in at 7.2 TB/s.  A few rows take a launch (3 us).
+// R = 1 / 2 / 4 / 8: 80 / 75 / 82 / 83).  Bound by memory: there 268 MB go out
+// and 168 MB come in, 97 MB of different rows and 71 MB of frequent ones that
+// several XCDs fetch, 5.8 TB/s.  A few rows take a launch (3 us).
 template <typename T, typename O>
 constexpr int kLookup = kVec<T> < kVec<O> ? kVec<T> : kVec<O>;   // 16 bytes at most on either side
 constexpr uint32_t kLookupTrips = 2;

@@ -272,9 +272,11 @@ __global__ __launch_bounds__(1024) void rms_norm_long_kernel(RmsNorm a)
 // ---------------------------------------------------------------- gradient
 // L lanes share a row; slot s of them takes rows s, s + slots, ... and keeps its
 // share of dw in registers, so dy, h and dh are read once for both gradients.  A
-// workgroup adds its slots' shares at the end and writes them to part_w.  Bound by memory: 16384 x 4096
-// bf16 94 us of 100 (537 MB, 5.7 TB/s), the rest joins the shares.  Nt: the
-// matrices by non-temporal accesses.
+// workgroup adds its slots' shares at the end and writes them to part_w.  The
+// weights' sums run in chains: a lane adds its rows' terms in turn, in float32,
+// at most rows / slots of them.  Bound by memory: 16384 x 4096 bf16 98 us (537
+// MB and 17 MB of shares, 5.7 TB/s), and 5 for the launch that joins the shares.
+// Nt: the matrices by non-temporal accesses.
 template <typename T, int L, int Ch, bool Nt>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void rms_norm_grad_kernel(RmsGrad a)
 {

@@ -433,9 +433,13 @@ int saps_merge(float *x, size_t n, const uint32_t *mask_words, const uint64_t *t
  *   - 16-bit inputs are widened to float32, sums and statistics are held in
  *     float32, and an output of 16 or 8 bits is rounded once, to nearest,
  *     ties to even.  Products and sums may be fused and are taken in a fixed
- *     order: the same call on the same inputs gives the same bits.
+ *     order: the same call on the same inputs gives the same bits.  Forms of
+ *     one operator may add in different orders: rms_norm's and rms_norm_q8's
+ *     rstd, distill_loss's and distill_loss_grad's loss and lse may part in
+ *     their last bits.
  *   - An operand's range for the overlap check goes from its first to its
  *     last element, the gaps between rows included; the gaps are not written.
+ *     So two ranges of columns of one matrix are refused where one is written.
  */
 enum gcq_type {
     GCQ_F32 = 0,
@@ -640,7 +644,11 @@ int rms_norm_grad(const void *dy, int type, size_t rows, size_t dim, size_t dy_l
  *
  * distill_loss gives loss and lse; distill_grad the gradient from a kept
  * lse (distill_loss's for the same logits and T; rows with s = 0 ignore it);
- * distill_loss_grad all three in one launch.
+ * distill_loss_grad all three in one launch.  A kept lse is rounded to float32,
+ * which moves distill_grad's q by up to 2^-24 |lse| relative (a row of nothing
+ * but the type's lowest value has no q left in it, nor has one whose lse
+ * overflows; weight such rows 0); distill_loss_grad takes q from the logits and
+ * does not depend on lse.
  * vocab 1 .. GCQ_LM_MAX_DIM, rows <= GCQ_LM_MAX_ROWS.
  * Errors: GCQ_ERR_PARAM, GCQ_ERR_NULL, GCQ_ERR_ALIGN, GCQ_ERR_OVERLAP,
  * GCQ_ERR_LAUNCH.
